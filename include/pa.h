@@ -19,6 +19,12 @@
  *   pa_importance        partition importance w_p = exp(LSE_p - LSE), averaged per
  *                        (query group, partition) -- DiTango, Methodology 1 ("Error
  *                        modelling", "Anchor steps": importance refreshed at anchors).
+ *   pa_attn_backward     gradients by q, k, v of the fresh pairs of such a merged output; the
+ *                        probabilities are computed again from q, k and the merged
+ *                        log-sum-exp.  The pages describe inference only.
+ *   pa_cache_store,      a K/V cache in 8 bits with a scale per block of tokens and head, and
+ *   pa_cache_attn        the attention state of queries against it, for prompts and single
+ *                        tokens.  The pages keep K and V at full width.
  *   pa_state_drift       per (query group, partition) sums of the squared change of the
  *                        states between two steps and of the reference states' squares:
  *                        the measurement behind the online prediction between anchor
@@ -79,14 +85,17 @@
  * one-line message for the last failure on that context (thread-unsafe per context).
  * Validation happens before anything is enqueued: on error nothing was launched.
  * Device-side waits are bounded; a wait that gives up records PA_ETIMEOUT in the
- * context's status word, which pa_sync_status reads (and clears).
+ * context's status word, which pa_sync_status reads (and clears).  So does a cache length or
+ * offset in device memory that lies outside the cache (PA_EINVAL).
  *
- * Alignment.  q, k, v, o_part, o and relayout src/dst must be 16-byte aligned;
- * lse_part, lse, w 4-byte aligned.
+ * Alignment.  q, k, v, o_part, o, gradients, cache codes, cache scratch and relayout src/dst
+ * must be 16-byte aligned; lse_part, lse, w, delta, cache scales, lengths and offsets 4-byte
+ * aligned.
  */
 #ifndef PA_H
 #define PA_H
 
+#include <stddef.h>
 #include <stdint.h>
 
 #ifdef __cplusplus
@@ -94,6 +103,7 @@ extern "C" {
 #endif
 
 #define PA_MAX_P 128
+#define PA_CACHE_BLOCK 64      /* tokens that share a scale in the 8-bit K/V cache */
 
 enum {
   PA_OK = 0,
@@ -123,7 +133,8 @@ void pa_destroy(pa_ctx* ctx);
 const char* pa_last_error(const pa_ctx* ctx);
 
 /* Synchronise `stream`, then read and clear the context's device status word.
- * Returns PA_OK, PA_ETIMEOUT if a kernel's bounded wait gave up, or PA_ECUDA. */
+ * Returns PA_OK, PA_ETIMEOUT if a kernel's bounded wait gave up, PA_EINVAL if a cache length
+ * or offset in device memory was out of range, or PA_ECUDA. */
 int pa_sync_status(pa_ctx* ctx, void* stream);
 
 /* pa_sync_status with a host-side deadline: poll `stream` (cudaStreamQuery) for up to
@@ -251,6 +262,99 @@ int pa_importance(pa_ctx* ctx, int B, int H, int N, int P, int G, const int32_t*
 int pa_state_drift(pa_ctx* ctx, pa_dtype dtype, int B, int H, int N, int D, int P, int G,
                    const int32_t* part_off, const uint8_t* sel, const void* o_new,
                    const void* o_ref, float* d2, float* r2, void* stream);
+
+/* ---------------------------------------------------------------- backward pass */
+typedef struct {
+  pa_dtype dtype;            /* of q, k, v, o, dout, dq, dk, dv */
+  int B, H, N, D;            /* D in {64, 128} */
+  float scale;
+  const void* q;             /* [B][H][N][D] */
+  const void* k;             /* [B][H][N][D] */
+  const void* v;             /* [B][H][N][D] */
+  const void* o;             /* [B][H][N][D] merged output (pa_merge_states) */
+  const float* lse;          /* [B][H][N]    merged log-sum-exp */
+  const void* dout;          /* [B][H][N][D] gradient of the loss by o */
+  const float* dlse;         /* [B][H][N]    gradient of the loss by lse, or NULL (0) */
+  int P;
+  const int32_t* part_off;   /* host, P+1 entries */
+  int G;
+  const uint8_t* fresh;      /* host, QG*KG entries; NULL = every pair fresh */
+  void* dq;                  /* [B][H][N][D] out, overwritten */
+  void* dk;                  /* [B][H][N][D] out, overwritten */
+  void* dv;                  /* [B][H][N][D] out, overwritten */
+  float* delta;              /* [B][H][N]    out: dout.o - dlse of every row */
+} pa_attn_bwd_desc;
+
+/* Gradients of pa_partition_attn followed by pa_merge_states with the same part_off, G, fresh
+ * and scale, given the merged (o, lse) and the loss's gradients by them.  Cached states that
+ * the merge took for the other pairs are constants; they enter through o and lse alone.  For
+ * query row i and key j of a fresh pair,
+ *   P_ij = exp(s_ij - lse_i) (0 where lse_i = -inf),  delta_i = dout_i . o_i - dlse_i,
+ *   dS_ij = P_ij (dout_i . v_j - delta_i),
+ *   dq_i = scale sum_j dS_ij k_j,  dk_j = scale sum_i dS_ij q_i,  dv_j = sum_i P_ij dout_i.
+ * Rows without a fresh pair get zeros.  Rows of pairs that are not fresh never reach a product,
+ * so they may hold anything.  Sums are fp32, in an order fixed by the sizes (no atomics: the
+ * same call gives the same bits); bf16 rounds P and dS to bf16 for the products.  delta is the
+ * only scratch, owned by the caller, so calls with their own delta may overlap and a captured
+ * graph keeps no library memory.  The outputs may not overlap the inputs or one another.
+ * Errors: PA_EINVAL, PA_EALIGN, PA_EUNSUPPORTED, PA_ECUDA. */
+int pa_attn_backward(pa_ctx* ctx, const pa_attn_bwd_desc* desc, void* stream);
+
+/* ---------------------------------------------------------------- 8-bit K/V cache */
+/* K and V of B requests and Hk heads as e4m3 codes [B][Hk][M][D] with one float32 scale per
+ * block of PA_CACHE_BLOCK tokens and head, [B][Hk][ceil(M / PA_CACHE_BLOCK)]: the value of a
+ * code is code * scale.  The scale is the smallest power of two 2^e with
+ * amax <= 448 * 2^e (amax over the block's finite values), e >= -126, and 0 for a block of
+ * zeros.  Infinities are stored as +-448, NaN stays NaN.  Neither needs initialising. */
+typedef struct {
+  pa_dtype dtype;            /* of k and v */
+  int B, Hk, T, M, D;        /* T new tokens into a cache of M (T <= M), D in {64, 128} */
+  const void* k;             /* [B][Hk][T][D] */
+  const void* v;             /* [B][Hk][T][D] */
+  const int32_t* start;      /* device [B]: token offset of the new rows; NULL = 0 */
+  void* k_codes;             /* [B][Hk][M][D] e4m3, in/out */
+  void* v_codes;             /* [B][Hk][M][D] e4m3, in/out */
+  float* k_scale;            /* [B][Hk][ceil(M / PA_CACHE_BLOCK)] in/out */
+  float* v_scale;            /* [B][Hk][ceil(M / PA_CACHE_BLOCK)] in/out */
+} pa_cache_store_desc;
+
+/* Store rows at tokens [start[b], start[b] + T) of request b's cache, as a prompt or a token
+ * at a time.  In a block that holds tokens before start[b], the scale becomes the larger of its
+ * own and the new rows' one, and the older codes are rounded again if it grew; tokens at or
+ * behind start[b] + T are not read and keep their codes, but not their meaning (the scale of
+ * the last block they share is replaced).  A start outside [0, M - T] leaves that request's cache as it was
+ * and records PA_EINVAL in the context's status word (pa_sync_status returns it).
+ * Errors: PA_EINVAL, PA_EALIGN, PA_EUNSUPPORTED, PA_ECUDA. */
+int pa_cache_store(pa_ctx* ctx, const pa_cache_store_desc* desc, void* stream);
+
+typedef struct {
+  pa_dtype dtype;            /* of q and o */
+  int B, H, Hk, Nq, M, D;    /* H a multiple of Hk; D in {64, 128} */
+  float scale;               /* softmax scale */
+  const void* q;             /* [B][H][Nq][D] */
+  const void* k_codes;       /* [B][Hk][M][D] */
+  const void* v_codes;       /* [B][Hk][M][D] */
+  const float* k_scale;      /* [B][Hk][ceil(M / PA_CACHE_BLOCK)] */
+  const float* v_scale;      /* [B][Hk][ceil(M / PA_CACHE_BLOCK)] */
+  const int32_t* lens;       /* device [B]: tokens held, 0..M; NULL = M */
+  void* o;                   /* [B][H][Nq][D] out */
+  float* lse;                /* [B][H][Nq]    out, natural log */
+  void* ws;                  /* scratch of ws_bytes bytes; may be NULL when none is needed */
+  size_t ws_bytes;           /* at least what pa_cache_attn_ws gives for these sizes */
+} pa_cache_attn_desc;
+
+/* Attention state of each query row against the first lens[b] tokens of its request's cache:
+ *   lse_i = ln sum_j exp(scale q_i . k_j),  o_i = sum_j exp(scale q_i . k_j - lse_i) v_j.
+ * Query head h reads KV head h / (H / Hk).  Tokens at or behind lens[b] and the scales of blocks
+ * behind it are not read; without any token o = 0, lse = -inf.  With P = 1 the result has the
+ * layout of pa_partition_attn's states, so pa_merge_states joins it with others.  The scratch
+ * belongs to the caller: calls that may overlap need one each.  A length outside [0, M] is
+ * clamped and records PA_EINVAL in the context's status word.  Results do not depend on the
+ * order in which blocks run.  Errors: PA_EINVAL, PA_EALIGN, PA_EUNSUPPORTED, PA_ECUDA. */
+int pa_cache_attn(pa_ctx* ctx, const pa_cache_attn_desc* desc, void* stream);
+
+/* Bytes of scratch that pa_cache_attn needs for these sizes (0 when none), on this device. */
+int pa_cache_attn_ws(pa_ctx* ctx, pa_dtype dtype, int B, int H, int Hk, int Nq, int M, int D, size_t* bytes);
 
 /* ---------------------------------------------------------------- bounded-wait self-test */
 /* Library diagnostics; the pages have no counterpart.  Every pipeline barrier wait in the

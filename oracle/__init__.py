@@ -38,6 +38,9 @@ What is computed, and where the pages state it (DiTango web summary, Methodology
   (diagonal) group's relative drift is the proxy.
 * relayout_seq2head -- the sequence-major -> head-major permutation that the Ulysses
   all-to-all performs, here on one device (SwiftFusion, Methodology 2).
+* attn_backward -- gradients of a merged output by q, k, v of its fresh pairs.
+* e4m3_round / cache_scale / cache_store / cache_values / cache_attn -- the 8-bit K/V cache
+  and attention over it.  The pages have neither a backward pass nor such a cache.
 
 Conventions: a partition with no valid keys has LSE_p = -inf and O_p = 0; a row whose
 states are all -inf merges to LSE = -inf, O = 0; importance of such a row is 0.
@@ -54,6 +57,8 @@ __all__ = [
     "partition_states", "merge_states", "merge_with_reuse", "importance",
     "select_fresh", "relayout_seq2head", "group_bounds", "compose_states",
     "merge_with_composed_cache", "state_drift", "predict_fresh",
+    "attn_backward", "selected_pairs", "e4m3_round", "cache_scale", "cache_store", "cache_values",
+    "cache_attn",
 ]
 
 
@@ -269,3 +274,94 @@ def relayout_seq2head(src, n_chunks=1):
         for h in range(H):
             dst[h, lo:hi, :] = src[lo:hi, h, :]
     return dst
+
+
+# ------------------------------------------------------------------ backward pass
+def attn_backward(q, k, v, o, lse, do, dlse, off, G, fresh, scale):
+    """Gradients (dq, dk, dv, delta) of the fresh pairs' share of a merged output, from its
+    definition: P = exp(s - lse), delta = do.o - dlse, dS = P (do.v - delta).  float64 arrays
+    [B, H, N, D], lse, dlse [B, H, N] (dlse may be None); fresh [QG, KG] or None."""
+    B, H, N, D = q.shape
+    delta = (do * o).sum(-1) - (0.0 if dlse is None else dlse)
+    sel = selected_pairs(off, G, fresh, N)
+    s = scale * np.einsum("bhid,bhjd->bhij", q, k)
+    with np.errstate(over="ignore", invalid="ignore"):
+        p = np.where(sel & ~np.isneginf(lse)[..., None], np.exp(s - lse[..., None]), 0.0)
+    ds = p * (np.einsum("bhid,bhjd->bhij", do, v) - delta[..., None])
+    return (scale * np.einsum("bhij,bhjd->bhid", ds, k), scale * np.einsum("bhij,bhid->bhjd", ds, q),
+            np.einsum("bhij,bhid->bhjd", p, do), delta)
+
+
+def selected_pairs(off, G, fresh, N):
+    """bool[N, N]: key j belongs to a KV group that row i's query group computes."""
+    P = len(off) - 1
+    bounds = [int(off[min(g * G, P)]) for g in range(-(-P // G) + 1)]
+    grp = np.searchsorted(bounds, np.arange(N), side="right") - 1
+    if fresh is None:
+        return np.ones((N, N), dtype=bool)
+    return np.asarray(fresh)[grp[:, None], grp[None, :]] != 0
+
+
+# ------------------------------------------------------------------ 8-bit K/V cache
+CACHE_BLOCK = 64
+
+
+def e4m3_round(x):
+    """Nearest e4m3 value (ties to even; 3 mantissa bits, exponents from -6, largest 448)."""
+    x = np.asarray(x, dtype=np.float64)
+    with np.errstate(invalid="ignore"):
+        e = np.floor(np.log2(np.maximum(np.where(np.isfinite(x), np.abs(x), 448.0), 2.0 ** -6)))
+        step = 2.0 ** (e - 3)
+        return np.clip(np.where(np.isinf(x), np.sign(x) * 448.0, np.rint(x / step) * step), -448.0, 448.0)
+
+
+def cache_scale(amax):
+    """Smallest 2^e, e >= -126, with amax <= 448 * 2^e; 0 for 0."""
+    if amax == 0:
+        return 0.0
+    m, e = np.frexp(amax)                       # amax = m * 2^e, 0.5 <= m < 1; 448 = 0.875 * 2^9
+    return float(2.0 ** max(int(e) - 9 + (m > 0.875), -126))
+
+
+def cache_store(x, start, codes, scale):
+    """New (codes, scale) after storing x [T, D] at token `start` of one head's cache: codes
+    [M, D] as e4m3 values, scale [ceil(M / 64)]."""
+    codes, scale = codes.copy(), scale.copy()
+    T = len(x)
+    for blk in range(start // CACHE_BLOCK, (start + T - 1) // CACHE_BLOCK + 1):
+        t0 = blk * CACHE_BLOCK
+        lo, hi = max(t0, start), min(t0 + CACHE_BLOCK, start + T)
+        rows = x[lo - start:hi - start]
+        amax = np.abs(rows[np.isfinite(rows)]).max(initial=0.0)
+        had = scale[blk] if t0 < start else 0.0
+        now = max(had, cache_scale(amax))
+        if t0 < start and now > had:
+            codes[t0:start] = e4m3_round(codes[t0:start] * (had / now))
+        codes[lo:hi] = e4m3_round(rows / (now if now > 0 else 1.0))
+        scale[blk] = now
+    return codes, scale
+
+
+def cache_values(codes, scale):
+    """The K or V that a cache [.., M, D] with scales [.., ceil(M / 64)] stands for."""
+    M = codes.shape[-2]
+    return codes * np.repeat(scale, CACHE_BLOCK, axis=-1)[..., :M, None]
+
+
+def cache_attn(q, k, v, lens, scale):
+    """(o, lse) of q [B, H, Nq, D] against the first lens[b] tokens of k, v [B, Hk, M, D]."""
+    B, H, Nq, D = q.shape
+    share = H // k.shape[1]
+    o, lse = np.zeros(q.shape), np.full((B, H, Nq), -np.inf)
+    for b in range(B):
+        n = int(lens[b])
+        if n == 0:
+            continue
+        for h in range(H):
+            s = scale * q[b, h] @ k[b, h // share, :n].T
+            m = s.max(axis=1, keepdims=True)
+            e = np.exp(s - m)
+            z = e.sum(axis=1, keepdims=True)
+            lse[b, h] = (m + np.log(z))[:, 0]
+            o[b, h] = (e / z) @ v[b, h // share, :n]
+    return o, lse

@@ -9,6 +9,7 @@ names follow the C ABI in ``include/pa.h``:
     pa_init / Context            pa_partition_attn    pa_merge_states
     pa_importance                pa_relayout_seq2head pa_sync_status / pa_wait_status
     pa_merge_states_noalloc      pa_compose_states    pa_state_drift
+    pa_attn_backward             pa_cache_store       pa_cache_attn
 
 There is no fallback: if ``libpa.so`` is missing or the device is not sm_100 the calls
 raise.
@@ -25,18 +26,21 @@ __all__ = [
     "pa_partition_attn", "pa_merge_states", "pa_importance", "pa_relayout_seq2head",
     "pa_merge_states_noalloc", "pa_compose_states", "pa_state_drift", "pa_selftest_wait", "EXPORTED",
     "pa_relayout_seq2head_at",
+    "pa_attn_backward", "pa_cache_store", "pa_cache_attn", "cache_attn_workspace", "PA_CACHE_BLOCK",
     "select_fresh",
     "predict_fresh",
 ]
 
 PA_F32, PA_BF16 = 0, 1
 PA_MAX_P = 128
+PA_CACHE_BLOCK = 64                     # tokens that share a scale in the 8-bit K/V cache
 _ERRORS = {-1: "PA_EINVAL", -2: "PA_EALIGN", -3: "PA_EUNSUPPORTED", -4: "PA_ENOMEM",
            -5: "PA_ECUDA", -6: "PA_ETIMEOUT"}
 EXPORTED = ("pa_init", "pa_destroy", "pa_last_error", "pa_sync_status", "pa_wait_status", "pa_version",
             "pa_partition_attn", "pa_merge_states", "pa_importance", "pa_relayout_seq2head",
             "pa_merge_states_noalloc", "pa_compose_states", "pa_state_drift", "pa_selftest_wait",
-            "pa_relayout_seq2head_at")
+            "pa_relayout_seq2head_at", "pa_attn_backward", "pa_cache_store", "pa_cache_attn",
+            "pa_cache_attn_ws")
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 
@@ -70,6 +74,34 @@ class _MergeDesc(ctypes.Structure):
                 ("w", ctypes.c_void_p), ("cached_per_group", ctypes.c_int)]
 
 
+class _AttnBwdDesc(ctypes.Structure):
+    _fields_ = [("dtype", ctypes.c_int), ("B", ctypes.c_int), ("H", ctypes.c_int),
+                ("N", ctypes.c_int), ("D", ctypes.c_int), ("scale", ctypes.c_float),
+                ("q", ctypes.c_void_p), ("k", ctypes.c_void_p), ("v", ctypes.c_void_p),
+                ("o", ctypes.c_void_p), ("lse", ctypes.c_void_p), ("dout", ctypes.c_void_p),
+                ("dlse", ctypes.c_void_p), ("P", ctypes.c_int), ("part_off", ctypes.c_void_p),
+                ("G", ctypes.c_int), ("fresh", ctypes.c_void_p), ("dq", ctypes.c_void_p),
+                ("dk", ctypes.c_void_p), ("dv", ctypes.c_void_p), ("delta", ctypes.c_void_p)]
+
+
+class _CacheStoreDesc(ctypes.Structure):
+    _fields_ = [("dtype", ctypes.c_int), ("B", ctypes.c_int), ("Hk", ctypes.c_int),
+                ("T", ctypes.c_int), ("M", ctypes.c_int), ("D", ctypes.c_int),
+                ("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("start", ctypes.c_void_p),
+                ("k_codes", ctypes.c_void_p), ("v_codes", ctypes.c_void_p),
+                ("k_scale", ctypes.c_void_p), ("v_scale", ctypes.c_void_p)]
+
+
+class _CacheAttnDesc(ctypes.Structure):
+    _fields_ = [("dtype", ctypes.c_int), ("B", ctypes.c_int), ("H", ctypes.c_int),
+                ("Hk", ctypes.c_int), ("Nq", ctypes.c_int), ("M", ctypes.c_int),
+                ("D", ctypes.c_int), ("scale", ctypes.c_float), ("q", ctypes.c_void_p),
+                ("k_codes", ctypes.c_void_p), ("v_codes", ctypes.c_void_p),
+                ("k_scale", ctypes.c_void_p), ("v_scale", ctypes.c_void_p),
+                ("lens", ctypes.c_void_p), ("o", ctypes.c_void_p), ("lse", ctypes.c_void_p),
+                ("ws", ctypes.c_void_p), ("ws_bytes", ctypes.c_size_t)]
+
+
 _LIB = None
 
 
@@ -100,9 +132,14 @@ def lib():
         L.pa_relayout_seq2head_at.argtypes = [vp, vp, vp, ci, ci, ci, ci, ci, ci, vp]
         L.pa_state_drift.argtypes = [vp, ci, ci, ci, ci, ci, ci, ci, vp, vp, vp, vp, vp, vp, vp]
         L.pa_selftest_wait.argtypes = [vp, ctypes.c_double, vp]
+        L.pa_attn_backward.argtypes = [vp, ctypes.POINTER(_AttnBwdDesc), vp]
+        L.pa_cache_store.argtypes = [vp, ctypes.POINTER(_CacheStoreDesc), vp]
+        L.pa_cache_attn.argtypes = [vp, ctypes.POINTER(_CacheAttnDesc), vp]
+        L.pa_cache_attn_ws.argtypes = [vp, ci, ci, ci, ci, ci, ci, ci, ctypes.POINTER(ctypes.c_size_t)]
         for f in ("pa_init", "pa_sync_status", "pa_wait_status", "pa_partition_attn", "pa_merge_states", "pa_merge_states_noalloc",
                   "pa_compose_states", "pa_state_drift", "pa_selftest_wait",
-                  "pa_importance", "pa_relayout_seq2head", "pa_relayout_seq2head_at"):
+                  "pa_importance", "pa_relayout_seq2head", "pa_relayout_seq2head_at",
+                  "pa_attn_backward", "pa_cache_store", "pa_cache_attn", "pa_cache_attn_ws"):
             getattr(L, f).restype = ci
         _LIB = L
     return _LIB
@@ -280,6 +317,118 @@ def pa_relayout_seq2head_at(ctx: Context, src, dst, tok0, stream=None):
     _check(ctx.ptr, lib().pa_relayout_seq2head_at(ctx.ptr, src.data_ptr(), dst.data_ptr(), n_tok, H, D,
                                                   src.element_size(), dst.shape[-2], int(tok0),
                                                   _stream(stream)))
+
+
+def _want(ctx, name, t, shape, dtype):
+    """Check a tensor argument: the kernels take raw pointers to contiguous device memory."""
+    if tuple(t.shape) != tuple(shape):
+        raise PAError(-1, f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    if t.dtype != dtype:
+        raise PAError(-3, f"{name} has dtype {t.dtype}, expected {dtype}")
+    if t.device.type != "cuda" or t.device.index != ctx.device:
+        raise PAError(-1, f"{name} is on {t.device}, the context on cuda:{ctx.device}")
+    if not t.is_contiguous():
+        raise PAError(-1, f"{name} is not contiguous")
+    return t.data_ptr()
+
+
+def pa_attn_backward(ctx: Context, q, k, v, o, lse, do, part_off, G, fresh, dq, dk, dv, delta,
+                     dlse=None, scale=None, stream=None):
+    """Gradients dq, dk, dv (overwritten, [B, H, N, D]) of the fresh pairs of a merged output
+    (o [B, H, N, D], lse [B, H, N]) from the loss's gradients do and, optionally, dlse.
+    Reused states are constants; a row without a fresh pair gets zeros.  delta [B, H, N] f32
+    receives do.o - dlse and is the call's only scratch.  part_off, G, fresh and scale as in
+    the forward call."""
+    import torch
+    B, H, N, D = q.shape
+    code = _dtype_code(q)
+    off, fr = _host_i32(part_off), _host_u8(fresh)
+    _want_mask(off, G, fr)
+    full, row = (B, H, N, D), (B, H, N)
+    ptrs = {n: _want(ctx, n, t, full, q.dtype) for n, t in
+            (("q", q), ("k", k), ("v", v), ("o", o), ("do", do), ("dq", dq), ("dk", dk), ("dv", dv))}
+    rows = {n: None if t is None else _want(ctx, n, t, row, torch.float32) for n, t in
+            (("lse", lse), ("dlse", dlse), ("delta", delta))}
+    d = _AttnBwdDesc(code, B, H, N, D, float(scale if scale is not None else 1.0 / np.sqrt(D)),
+                     ptrs["q"], ptrs["k"], ptrs["v"], ptrs["o"], rows["lse"], ptrs["do"], rows["dlse"],
+                     len(off) - 1, off.ctypes.data, int(G), None if fr is None else fr.ctypes.data,
+                     ptrs["dq"], ptrs["dk"], ptrs["dv"], rows["delta"])
+    _check(ctx.ptr, lib().pa_attn_backward(ctx.ptr, ctypes.byref(d), _stream(stream)))
+
+
+def _want_mask(off, G, fr):
+    """The C call reads P + 1 offsets and ceil(P / G)^2 mask entries."""
+    P = len(off) - 1
+    if off.ndim != 1 or P < 1 or not 1 <= int(G) <= P:
+        raise PAError(-1, f"part_off of {off.size} entries with G={G}")
+    QG = -(-P // int(G))
+    if fr is not None and fr.size != QG * QG:
+        raise PAError(-1, f"fresh has {fr.size} entries, expected {QG} x {QG}")
+
+
+def _cache_shapes(ctx, kc, vc, k_scale, v_scale):
+    import torch
+    B, Hk, M, D = kc.shape
+    code = torch.uint8 if kc.dtype == torch.uint8 else torch.float8_e4m3fn
+    blocks = (B, Hk, -(-M // PA_CACHE_BLOCK))
+    return (B, Hk, M, D, _want(ctx, "kc", kc, (B, Hk, M, D), code), _want(ctx, "vc", vc, (B, Hk, M, D), code),
+            _want(ctx, "k_scale", k_scale, blocks, torch.float32),
+            _want(ctx, "v_scale", v_scale, blocks, torch.float32))
+
+
+def pa_cache_store(ctx: Context, k, v, start, kc, vc, k_scale, v_scale, stream=None):
+    """Round k, v [B, Hk, T, D] (bf16 or f32) into the 8-bit cache kc, vc [B, Hk, M, D]
+    (float8_e4m3fn, or uint8 holding the codes) with scales [B, Hk, ceil(M / 64)] f32, at token
+    offsets start (int32 [B] on the device, or None for 0)."""
+    import torch
+    B, Hk, M, D, pk, pv, pks, pvs = _cache_shapes(ctx, kc, vc, k_scale, v_scale)
+    T = k.shape[2] if k.dim() == 4 else -1
+    code = _dtype_code(k)
+    d = _CacheStoreDesc(code, B, Hk, T, M, D, _want(ctx, "k", k, (B, Hk, T, D), k.dtype),
+                        _want(ctx, "v", v, (B, Hk, T, D), k.dtype),
+                        None if start is None else _want(ctx, "start", start, (B,), torch.int32),
+                        pk, pv, pks, pvs)
+    _check(ctx.ptr, lib().pa_cache_store(ctx.ptr, ctypes.byref(d), _stream(stream)))
+
+
+def cache_attn_workspace(ctx: Context, q, kc):
+    """Scratch for pa_cache_attn on tensors of these shapes (uint8, maybe empty).  Calls that
+    may overlap on the GPU, and captured graphs that may, need one each."""
+    import torch
+    B, H, Nq, D = q.shape
+    n = ctypes.c_size_t()
+    _check(ctx.ptr, lib().pa_cache_attn_ws(ctx.ptr, _dtype_code(q), B, H, kc.shape[1], Nq, kc.shape[2], D,
+                                           ctypes.byref(n)))
+    return torch.empty(n.value, dtype=torch.uint8, device=torch.device("cuda", ctx.device))
+
+
+def pa_cache_attn(ctx: Context, q, kc, vc, k_scale, v_scale, lens, o, lse, scale=None, workspace=None,
+                  stream=None):
+    """Attention state (o [B, H, Nq, D], lse [B, H, Nq] f32) of q against the first lens[b]
+    tokens (int32 [B] on the device, or None for all M) of the 8-bit cache; H is a multiple of
+    the cache's Hk.  workspace: from cache_attn_workspace; without one the call takes it from
+    torch's allocator."""
+    import torch
+    B, Hk, M, D, pk, pv, pks, pvs = _cache_shapes(ctx, kc, vc, k_scale, v_scale)
+    if q.dim() != 4:
+        raise PAError(-1, f"q has shape {tuple(q.shape)}, expected [B, H, Nq, D]")
+    H, Nq = q.shape[1], q.shape[2]
+    code = _dtype_code(q)
+    pq = _want(ctx, "q", q, (B, H, Nq, D), q.dtype)
+    s = _stream(stream)
+    if workspace is None:
+        workspace = cache_attn_workspace(ctx, q, kc)
+        if workspace.numel():
+            # allocated for the current stream: not handed out again before `s` is done with it
+            workspace.record_stream(torch.cuda.ExternalStream(s, device=workspace.device))
+    else:
+        _want(ctx, "workspace", workspace, (workspace.numel(),), torch.uint8)
+    d = _CacheAttnDesc(code, B, H, Hk, Nq, M, D, float(scale if scale is not None else 1.0 / np.sqrt(D)),
+                       pq, pk, pv, pks, pvs,
+                       None if lens is None else _want(ctx, "lens", lens, (B,), torch.int32),
+                       _want(ctx, "o", o, (B, H, Nq, D), q.dtype), _want(ctx, "lse", lse, (B, H, Nq), torch.float32),
+                       workspace.data_ptr() if workspace.numel() else None, workspace.numel())
+    _check(ctx.ptr, lib().pa_cache_attn(ctx.ptr, ctypes.byref(d), s))
 
 
 def select_fresh(w_stored, G: int, threshold: float) -> np.ndarray:

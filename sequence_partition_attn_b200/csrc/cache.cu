@@ -1,0 +1,159 @@
+// cache.cu -- the 8-bit K/V cache: e4m3 codes [B][Hk][M][D] with one scale per block of 64
+// tokens and head, [B][Hk][ceil(M / 64)].
+//
+// A block's scale is the smallest power of two 2^e with amax <= 448 * 2^e (448 is the largest
+// e4m3 value), e >= -126, and 0 for a block of zeros.  A power of two makes x / scale exact, so
+// each code is one rounding (at most 2^-4 relative, half an e4m3 step), independent of how the
+// division is done; and since e4m3 keeps its 3 mantissa bits at every exponent, a scale
+// that is not amax / 448 itself costs no precision, only the unused top of the range.
+//
+// Storing rows behind a block's earlier tokens keeps the larger of the two scales.  If the
+// scale grows, the older codes are rounded once more to the new one, which is exact unless they
+// fall below e4m3's normal range.
+#include <cuda_fp8.h>
+
+#include "pa_device.cuh"
+#include "pa_launch.h"
+
+namespace pa {
+namespace {
+
+constexpr int kTok = PA_CACHE_BLOCK;
+constexpr int kThreads = 256;
+constexpr int kSeg = 16;              // channels per item: one 16-byte code store
+
+template <typename T>
+__device__ __forceinline__ void load16(const T* p, float (&x)[kSeg]);
+template <>
+__device__ __forceinline__ void load16<float>(const float* p, float (&x)[kSeg]) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float4 v = __ldg(reinterpret_cast<const float4*>(p) + i);
+    x[4 * i] = v.x; x[4 * i + 1] = v.y; x[4 * i + 2] = v.z; x[4 * i + 3] = v.w;
+  }
+}
+template <>
+__device__ __forceinline__ void load16<__nv_bfloat16>(const __nv_bfloat16* p, float (&x)[kSeg]) {
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const uint4 v = __ldg(reinterpret_cast<const uint4*>(p) + i);
+    const uint32_t u[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      x[8 * i + 2 * j] = __uint_as_float(u[j] << 16);
+      x[8 * i + 2 * j + 1] = __uint_as_float(u[j] & 0xFFFF0000u);
+    }
+  }
+}
+
+// Smallest 2^e >= amax / 448 with e >= -126 (amax > 0, finite): 448 = 1.75 * 2^8.
+__device__ __forceinline__ float block_scale(float amax) {
+  const uint32_t u = __float_as_uint(amax);
+  int e = static_cast<int>(u >> 23) - 127 - 8 + ((u & 0x7FFFFFu) > 0x600000u ? 1 : 0);
+  e = max(e, -126);                   // subnormal amax: u >> 23 is 0, below the limit anyway
+  return __uint_as_float(static_cast<uint32_t>(e + 127) << 23);
+}
+
+__device__ __forceinline__ uint4 encode16(const float (&x)[kSeg], float inv) {
+  uint32_t w[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const __nv_fp8x2_storage_t lo = __nv_cvt_float2_to_fp8x2(make_float2(x[4 * i] * inv, x[4 * i + 1] * inv), __NV_SATFINITE, __NV_E4M3);
+    const __nv_fp8x2_storage_t hi = __nv_cvt_float2_to_fp8x2(make_float2(x[4 * i + 2] * inv, x[4 * i + 3] * inv), __NV_SATFINITE, __NV_E4M3);
+    w[i] = static_cast<uint32_t>(lo) | (static_cast<uint32_t>(hi) << 16);
+  }
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+__device__ __forceinline__ void decode16(uint4 c, float (&x)[kSeg]) {
+  const uint32_t w[4] = {c.x, c.y, c.z, c.w};
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(w[i >> 1] >> (16 * (i & 1))), __NV_E4M3);
+    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h));
+    x[2 * i] = f.x;
+    x[2 * i + 1] = f.y;
+  }
+}
+
+// One block of threads per cache block that the new rows touch, for K or V of one head.  Bound
+// by HBM: the rows are read once into registers, reduced, and written as codes.
+template <typename T, int D>
+__global__ void __launch_bounds__(kThreads) cache_store_kernel(const __grid_constant__ CacheStoreParams prm) {
+  constexpr int kSegs = D / kSeg;
+  constexpr int kItems = kTok * kSegs / kThreads;      // (token, 16 channels) items per thread
+  __shared__ float s_max[kThreads / 32];
+  const int i = blockIdx.x % prm.touched;
+  const int kv = (blockIdx.x / prm.touched) & 1;
+  const int bh = blockIdx.x / prm.touched / 2;
+  const int b = bh / prm.Hk;
+  const int t0 = prm.start ? prm.start[b] : 0;
+  if (t0 < 0 || t0 > prm.M - prm.T) {                  // the rows do not fit: leave the request's cache alone
+    if (threadIdx.x == 0) atomicExch(prm.status, PA_EINVAL);
+    return;
+  }
+  const int blk = t0 / kTok + i;
+  const int tok0 = blk * kTok;
+  if (tok0 >= t0 + prm.T) return;
+  const T* src = static_cast<const T*>(kv ? prm.v : prm.k) + static_cast<size_t>(bh) * prm.T * D;
+  uint8_t* codes = static_cast<uint8_t*>(kv ? prm.v_codes : prm.k_codes) + (static_cast<size_t>(bh) * prm.M + tok0) * D;
+  float* scale = (kv ? prm.v_scale : prm.k_scale) + static_cast<size_t>(bh) * prm.blocks + blk;
+  const float had = tok0 < t0 ? *scale : 0.0f;
+
+  float x[kItems][kSeg];
+  float amax = 0.0f;
+#pragma unroll
+  for (int n = 0; n < kItems; ++n) {
+    const int idx = n * kThreads + threadIdx.x;
+    const int row = tok0 + idx / kSegs - t0;
+    if (row < 0 || row >= prm.T) continue;
+    load16<T>(src + static_cast<size_t>(row) * D + (idx % kSegs) * kSeg, x[n]);
+#pragma unroll
+    for (int c = 0; c < kSeg; ++c) {
+      const float a = fabsf(x[n][c]);
+      if (a < INFINITY) amax = fmaxf(amax, a);         // infinities saturate, NaN stays NaN: neither sets the scale
+    }
+  }
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, off));
+  if ((threadIdx.x & 31) == 0) s_max[threadIdx.x >> 5] = amax;
+  __syncthreads();                                     // also: every thread has read *scale
+  amax = s_max[0];
+#pragma unroll
+  for (int w = 1; w < kThreads / 32; ++w) amax = fmaxf(amax, s_max[w]);
+  const float need = amax > 0.0f ? block_scale(amax) : 0.0f;
+  const float now = fmaxf(had, need);
+  // 1 / now is a power of two too: exact, in range for every e in [-126, 120]
+  const float inv = now > 0.0f ? 1.0f / now : 1.0f;
+#pragma unroll
+  for (int n = 0; n < kItems; ++n) {
+    const int idx = n * kThreads + threadIdx.x;
+    const int tok = idx / kSegs;
+    const int row = tok0 + tok - t0;
+    uint4* dst = reinterpret_cast<uint4*>(codes + static_cast<size_t>(tok) * D + (idx % kSegs) * kSeg);
+    if (row >= 0 && row < prm.T) {
+      *dst = encode16(x[n], inv);
+    } else if (row < 0 && now > had) {
+      float old[kSeg];
+      decode16(*dst, old);
+      *dst = encode16(old, had * inv);
+    }
+  }
+  if (threadIdx.x == 0) *scale = now;
+}
+
+template <typename T, int D>
+int store_impl(const CacheStoreParams& prm, unsigned blocks, cudaStream_t st) {
+  cache_store_kernel<T, D><<<blocks, kThreads, 0, st>>>(prm);
+  return static_cast<int>(cudaGetLastError());
+}
+
+}  // namespace
+
+int launch_cache_store(const CacheStoreParams& prm, unsigned blocks, int dtype, int D, cudaStream_t st) {
+  if (dtype == PA_BF16)
+    return D == 64 ? store_impl<__nv_bfloat16, 64>(prm, blocks, st) : store_impl<__nv_bfloat16, 128>(prm, blocks, st);
+  return D == 64 ? store_impl<float, 64>(prm, blocks, st) : store_impl<float, 128>(prm, blocks, st);
+}
+
+}  // namespace pa

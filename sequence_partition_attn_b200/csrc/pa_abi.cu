@@ -359,6 +359,7 @@ static int read_status(pa_ctx* ctx) {
   if (e != cudaSuccess) return cuda_fail(ctx, e, "status read");
   if (h != 0) {
     cudaMemset(ctx->d_status, 0, sizeof(int));
+    if (h == PA_EINVAL) return fail(ctx, PA_EINVAL, "a cache length or offset in device memory is outside the cache");
     return fail(ctx, PA_ETIMEOUT, "a device-side wait gave up (status %d)", h);
   }
   return PA_OK;
@@ -669,6 +670,186 @@ static int pa_relayout_seq2head_at_impl(pa_ctx* ctx, const void* src, void* dst,
   return e ? cuda_fail(ctx, e, "relayout launch") : PA_OK;
 }
 
+// Row tiles of the backward pass per owner group.  Unlike the forward's, groups without a fresh
+// pair are kept: their gradients are written as zeros.
+static int fill_owner_tiles(pa::AttnTables& t, int tile_rows) {
+  int acc = 0;
+  for (int g = 0; g < t.QG; ++g) {
+    t.tile_start[g] = acc;
+    acc += (t.qg_row0[g + 1] - t.qg_row0[g] + tile_rows - 1) / tile_rows;
+  }
+  t.tile_start[t.QG] = acc;
+  return acc;
+}
+
+static int pa_attn_backward_impl(pa_ctx* ctx, const pa_attn_bwd_desc* d, void* stream) {
+  if (!ctx) return fail(nullptr, PA_EINVAL, "ctx is NULL");
+  if (!d) return fail(ctx, PA_EINVAL, "desc is NULL");
+  if (d->dtype != PA_BF16 && d->dtype != PA_F32) return fail(ctx, PA_EUNSUPPORTED, "dtype %d", (int)d->dtype);
+  if (d->D != 64 && d->D != 128) return fail(ctx, PA_EUNSUPPORTED, "D=%d (supported: 64, 128)", d->D);
+  if (d->B < 1 || d->H < 1 || d->N < 0) return fail(ctx, PA_EINVAL, "B=%d H=%d N=%d", d->B, d->H, d->N);
+  const long long BH = static_cast<long long>(d->B) * d->H;
+  if (BH > 65535) return fail(ctx, PA_EINVAL, "B*H=%lld exceeds 65535", BH);
+  if (!(d->scale > 0.0f) || !(d->scale < 1e30f)) return fail(ctx, PA_EINVAL, "scale must be positive and finite");
+  pa::BwdParams prm;
+  memset(&prm, 0, sizeof prm);
+  int rc = build_tables(ctx, d->N, d->P, d->G, d->part_off, d->fresh, prm.tq);
+  if (rc) return rc;
+  if (d->N == 0) return PA_OK;
+  if (!d->q || !d->k || !d->v || !d->o || !d->lse || !d->dout || !d->dq || !d->dk || !d->dv || !d->delta)
+    return fail(ctx, PA_EINVAL, "null tensor pointer");
+  if (!aligned(d->q, 16) || !aligned(d->k, 16) || !aligned(d->v, 16) || !aligned(d->o, 16) || !aligned(d->dout, 16) ||
+      !aligned(d->dq, 16) || !aligned(d->dk, 16) || !aligned(d->dv, 16))
+    return fail(ctx, PA_EALIGN, "q, k, v, o and the gradients must be 16-byte aligned");
+  if (!aligned(d->lse, 4) || !aligned(d->delta, 4) || (d->dlse && !aligned(d->dlse, 4)))
+    return fail(ctx, PA_EALIGN, "lse, dlse and delta must be 4-byte aligned");
+  if ((rc = check_device(ctx))) return rc;
+  // The same table with keys as owners: KV group g streams the query partitions it is fresh for.
+  prm.tk = prm.tq;
+  memset(prm.tk.fresh_bits, 0, sizeof prm.tk.fresh_bits);
+  for (int p = 0; p < d->P; ++p)
+    for (int kg = 0; kg < prm.tq.QG; ++kg)
+      if (!d->fresh || d->fresh[(p / d->G) * prm.tq.QG + kg]) prm.tk.fresh_bits[kg][p >> 5] |= 1u << (p & 31);
+  merge_equal_groups(prm.tq);
+  merge_equal_groups(prm.tk);
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  prm.q = d->q;
+  prm.k = d->k;
+  prm.v = d->v;
+  prm.dout = d->dout;
+  prm.lse = d->lse;
+  prm.delta = d->delta;
+  prm.dq = d->dq;
+  prm.dk = d->dk;
+  prm.dv = d->dv;
+  prm.BH = (int)BH;
+  prm.N = d->N;
+  prm.D = d->D;
+  prm.scale = d->scale;
+  const int tile = pa::attn_bwd_fma_tile_rows();
+  prm.tiles_q = fill_owner_tiles(prm.tq, tile);
+  prm.tiles_k = fill_owner_tiles(prm.tk, tile);
+  const long long rows = BH * d->N;
+  if (rows > 0x7fffffffLL * 8) return fail(ctx, PA_EINVAL, "too many rows");
+  int e = pa::launch_delta(d->o, d->dout, d->dlse, d->delta, rows, d->D, d->dtype, st);
+  if (e) return cuda_fail(ctx, e, "delta launch");
+  e = pa::launch_attn_bwd_fma(prm, d->dtype, st);
+  return e ? cuda_fail(ctx, e, "attention backward launch") : PA_OK;
+}
+
+static int pa_cache_store_impl(pa_ctx* ctx, const pa_cache_store_desc* d, void* stream) {
+  if (!ctx) return fail(nullptr, PA_EINVAL, "ctx is NULL");
+  if (!d) return fail(ctx, PA_EINVAL, "desc is NULL");
+  if (d->dtype != PA_BF16 && d->dtype != PA_F32) return fail(ctx, PA_EUNSUPPORTED, "dtype %d", (int)d->dtype);
+  if (d->D != 64 && d->D != 128) return fail(ctx, PA_EUNSUPPORTED, "D=%d (supported: 64, 128)", d->D);
+  if (d->B < 1 || d->Hk < 1 || d->T < 0 || d->M < 1) return fail(ctx, PA_EINVAL, "B=%d Hk=%d T=%d M=%d", d->B, d->Hk, d->T, d->M);
+  if (d->T > d->M) return fail(ctx, PA_EINVAL, "T=%d rows do not fit a cache of M=%d", d->T, d->M);
+  if (d->T == 0) return PA_OK;
+  if (!d->k || !d->v || !d->k_codes || !d->v_codes || !d->k_scale || !d->v_scale)
+    return fail(ctx, PA_EINVAL, "null tensor pointer");
+  if (!aligned(d->k, 16) || !aligned(d->v, 16) || !aligned(d->k_codes, 16) || !aligned(d->v_codes, 16))
+    return fail(ctx, PA_EALIGN, "k, v and the codes must be 16-byte aligned");
+  if (!aligned(d->k_scale, 4) || !aligned(d->v_scale, 4) || (d->start && !aligned(d->start, 4)))
+    return fail(ctx, PA_EALIGN, "scales and start must be 4-byte aligned");
+  pa::CacheStoreParams prm;
+  memset(&prm, 0, sizeof prm);
+  prm.blocks = (d->M - 1) / PA_CACHE_BLOCK + 1;
+  // T rows at an unknown offset touch at most this many blocks; at offset 0 exactly ceil(T / block)
+  prm.touched = d->start ? static_cast<int>((static_cast<long long>(d->T) + PA_CACHE_BLOCK - 2) / PA_CACHE_BLOCK + 1)
+                         : (d->T - 1) / PA_CACHE_BLOCK + 1;
+  if (prm.touched > prm.blocks) prm.touched = prm.blocks;
+  const long long grid = 2LL * d->B * d->Hk * prm.touched;
+  if (static_cast<long long>(d->B) * d->Hk > 0x7fffffffLL / 2 || grid > 0x7fffffffLL)
+    return fail(ctx, PA_EINVAL, "too many cache blocks");
+  int rc = check_device(ctx);
+  if (rc) return rc;
+  prm.k = d->k;
+  prm.v = d->v;
+  prm.start = d->start;
+  prm.k_codes = d->k_codes;
+  prm.v_codes = d->v_codes;
+  prm.k_scale = d->k_scale;
+  prm.v_scale = d->v_scale;
+  prm.status = ctx->d_status;
+  prm.Hk = d->Hk;
+  prm.T = d->T;
+  prm.M = d->M;
+  int e = pa::launch_cache_store(prm, static_cast<unsigned>(grid), d->dtype, d->D, static_cast<cudaStream_t>(stream));
+  return e ? cuda_fail(ctx, e, "cache store launch") : PA_OK;
+}
+
+// Sizes and the split of the token axis of pa_cache_attn: a rule on sizes alone, so that the
+// scratch can be sized beforehand and a captured call replays with other lengths.
+static int plan_cache_attn(pa_ctx* ctx, pa_dtype dtype, int B, int H, int Hk, int Nq, int M, int D,
+                           pa::CacheAttnParams& prm, size_t* ws_bytes) {
+  if (dtype != PA_BF16 && dtype != PA_F32) return fail(ctx, PA_EUNSUPPORTED, "dtype %d", (int)dtype);
+  if (D != 64 && D != 128) return fail(ctx, PA_EUNSUPPORTED, "D=%d (supported: 64, 128)", D);
+  if (B < 1 || H < 1 || Hk < 1 || Nq < 0 || M < 1)
+    return fail(ctx, PA_EINVAL, "B=%d H=%d Hk=%d Nq=%d M=%d", B, H, Hk, Nq, M);
+  if (H % Hk) return fail(ctx, PA_EINVAL, "H=%d is not a multiple of Hk=%d", H, Hk);
+  const long long R = static_cast<long long>(H / Hk) * Nq, BHk = static_cast<long long>(B) * Hk;
+  if (BHk > 65535) return fail(ctx, PA_EINVAL, "B*Hk=%lld exceeds 65535", BHk);
+  if (R > 0x7fffffffLL - 1024) return fail(ctx, PA_EINVAL, "too many query rows for a KV head");
+  if (M > 0x7fffffff - 1024) return fail(ctx, PA_EINVAL, "M=%d too large", M);
+  memset(&prm, 0, sizeof prm);
+  prm.B = B;
+  prm.Hk = Hk;
+  prm.R = static_cast<int>(R);
+  prm.M = M;
+  prm.D = D;
+  prm.blocks = (M - 1) / PA_CACHE_BLOCK + 1;
+  prm.rows = R * BHk;
+  const long long tiles = BHk * ((R + pa::cache_attn_fma_tile_rows() - 1) / pa::cache_attn_fma_tile_rows());
+  long long splits = tiles > 0 ? 4LL * ctx->sm_count / tiles : 1;
+  splits = std::max(1LL, std::min(splits, static_cast<long long>(prm.blocks) / 4));
+  const long long blocks_per = (prm.blocks + splits - 1) / splits;
+  prm.chunk = static_cast<int>(blocks_per) * PA_CACHE_BLOCK;
+  prm.splits = static_cast<int>((prm.blocks + blocks_per - 1) / blocks_per);
+  if (prm.rows > 0x7fffffffLL) return fail(ctx, PA_EINVAL, "too many query rows");
+  *ws_bytes = prm.splits > 1 ? static_cast<size_t>(prm.splits) * prm.rows * (D + 1) * sizeof(float) : 0;
+  return PA_OK;
+}
+
+static int pa_cache_attn_impl(pa_ctx* ctx, const pa_cache_attn_desc* d, void* stream) {
+  if (!ctx) return fail(nullptr, PA_EINVAL, "ctx is NULL");
+  if (!d) return fail(ctx, PA_EINVAL, "desc is NULL");
+  if (!(d->scale > 0.0f) || !(d->scale < 1e30f)) return fail(ctx, PA_EINVAL, "scale must be positive and finite");
+  pa::CacheAttnParams prm;
+  size_t need = 0;
+  int rc = plan_cache_attn(ctx, d->dtype, d->B, d->H, d->Hk, d->Nq, d->M, d->D, prm, &need);
+  if (rc) return rc;
+  if (d->Nq == 0) return PA_OK;
+  if (!d->q || !d->k_codes || !d->v_codes || !d->k_scale || !d->v_scale || !d->o || !d->lse)
+    return fail(ctx, PA_EINVAL, "null tensor pointer");
+  if (need > 0 && (!d->ws || d->ws_bytes < need))
+    return fail(ctx, PA_EINVAL, "scratch of %zu bytes, %zu needed (pa_cache_attn_ws)", d->ws ? d->ws_bytes : 0, need);
+  if (!aligned(d->q, 16) || !aligned(d->o, 16) || !aligned(d->k_codes, 16) || !aligned(d->v_codes, 16) ||
+      (need > 0 && !aligned(d->ws, 16)))
+    return fail(ctx, PA_EALIGN, "q, o, the codes and the scratch must be 16-byte aligned");
+  if (!aligned(d->k_scale, 4) || !aligned(d->v_scale, 4) || !aligned(d->lse, 4) || (d->lens && !aligned(d->lens, 4)))
+    return fail(ctx, PA_EALIGN, "scales, lse and lens must be 4-byte aligned");
+  if ((rc = check_device(ctx))) return rc;
+  prm.q = d->q;
+  prm.k_codes = static_cast<const uint8_t*>(d->k_codes);
+  prm.v_codes = static_cast<const uint8_t*>(d->v_codes);
+  prm.k_scale = d->k_scale;
+  prm.v_scale = d->v_scale;
+  prm.lens = d->lens;
+  prm.o = d->o;
+  prm.lse = d->lse;
+  prm.status = ctx->d_status;
+  prm.scale = d->scale;
+  if (need > 0) {
+    prm.ws_o = static_cast<float*>(d->ws);
+    prm.ws_lse = prm.ws_o + static_cast<size_t>(prm.splits) * prm.rows * d->D;
+  }
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  int e = pa::launch_cache_attn_fma(prm, d->dtype, st);
+  if (e) return cuda_fail(ctx, e, "cache attention launch");
+  if (prm.splits > 1) e = pa::launch_cache_join(prm, d->dtype, st);
+  return e ? cuda_fail(ctx, e, "cache join launch") : PA_OK;
+}
+
 // With PA_DEBUG set when the context was created, every call synchronises its stream after
 // launching and returns what pa_sync_status finds (a launch or runtime error, or a
 // bounded device-side wait that gave up).
@@ -711,6 +892,25 @@ int pa_relayout_seq2head_at(pa_ctx* ctx, const void* src, void* dst, int n_tok, 
                             int dst_tokens, int dst_tok0, void* stream) {
   return debug_finish(ctx, stream, pa_relayout_seq2head_at_impl(ctx, src, dst, n_tok, H, D, elem_bytes, dst_tokens,
                                                                 dst_tok0, stream));
+}
+
+int pa_attn_backward(pa_ctx* ctx, const pa_attn_bwd_desc* d, void* stream) {
+  return debug_finish(ctx, stream, pa_attn_backward_impl(ctx, d, stream));
+}
+
+int pa_cache_store(pa_ctx* ctx, const pa_cache_store_desc* d, void* stream) {
+  return debug_finish(ctx, stream, pa_cache_store_impl(ctx, d, stream));
+}
+
+int pa_cache_attn(pa_ctx* ctx, const pa_cache_attn_desc* d, void* stream) {
+  return debug_finish(ctx, stream, pa_cache_attn_impl(ctx, d, stream));
+}
+
+int pa_cache_attn_ws(pa_ctx* ctx, pa_dtype dtype, int B, int H, int Hk, int Nq, int M, int D, size_t* bytes) {
+  if (!ctx) return fail(nullptr, PA_EINVAL, "ctx is NULL");
+  if (!bytes) return fail(ctx, PA_EINVAL, "bytes is NULL");
+  pa::CacheAttnParams prm;
+  return plan_cache_attn(ctx, dtype, B, H, Hk, Nq, M, D, prm, bytes);
 }
 
 int pa_selftest_wait(pa_ctx* ctx, double seconds, void* stream) {

@@ -360,3 +360,89 @@ struct ReducePairParams {
   int blk_start[PA_MAX_P + 1];
 };
 }  // namespace pa
+
+namespace pa {
+// ------------------------------------------------------------------ backward, 8-bit cache
+// Attention's backward pass.  tq: query groups as owners of row tiles, fresh_bits[g] the KV
+// partitions of their fresh pairs; tk: KV groups as owners, fresh_bits[g] the query partitions.
+struct BwdParams {
+  const void* q;
+  const void* k;
+  const void* v;
+  const void* dout;
+  const float* lse;               // [B][H][N] merged
+  const float* delta;             // [B][H][N] dO.O - dLSE
+  void* dq;
+  void* dk;
+  void* dv;
+  int BH, N, D;
+  int tiles_q, tiles_k;           // owner tiles per (b, h)
+  float scale;
+  AttnTables tq, tk;
+};
+
+struct CacheStoreParams {
+  const void* k;                  // [B][Hk][T][D]
+  const void* v;
+  const int32_t* start;           // [B] or null (0)
+  void* k_codes;                  // [B][Hk][M][D]
+  void* v_codes;
+  float* k_scale;                 // [B][Hk][blocks]
+  float* v_scale;
+  int* status;
+  int Hk, T, M, blocks;
+  int touched;                    // cache blocks that T rows can touch
+};
+
+struct CacheAttnParams {
+  const void* q;                  // [B][Hk][R][D]
+  const uint8_t* k_codes;
+  const uint8_t* v_codes;
+  const float* k_scale;
+  const float* v_scale;
+  const int32_t* lens;            // [B] or null (M)
+  void* o;
+  float* lse;
+  float* ws_o;                    // [splits][B * Hk * R][D] when splits > 1
+  float* ws_lse;                  // [splits][B * Hk * R]
+  int* status;
+  long long rows;                 // B * Hk * R
+  int B, Hk, R, M, D, blocks;
+  int splits, chunk;              // tokens per split, a multiple of the cache block
+  float scale;
+};
+
+// The maximal run of selected partitions at or after `from` that holds tokens, as the token
+// range [s0, s1) (neighbouring partitions join); returns where to go on.  s0 == s1 at the end.
+__device__ __forceinline__ int next_range(const AttnTables& t, int g, int from, int& s0, int& s1) {
+  s0 = s1 = 0;
+  int p = from;
+  while (p < t.P && !(fresh_bit(t.fresh_bits, g, p) && t.part_off[p + 1] > t.part_off[p])) ++p;
+  if (p == t.P) return p;
+  s0 = t.part_off[p];
+  while (p < t.P && (fresh_bit(t.fresh_bits, g, p) || t.part_off[p + 1] == t.part_off[p])) ++p;
+  s1 = t.part_off[p];
+  return p;
+}
+
+// Tokens held by request b's cache; a length outside [0, M] is recorded and clamped.
+__device__ __forceinline__ int cache_len(const CacheAttnParams& prm, int b) {
+  if (!prm.lens) return prm.M;
+  const int n = prm.lens[b];
+  if (n >= 0 && n <= prm.M) return n;
+  if (threadIdx.x == 0) atomicExch(prm.status, PA_EINVAL);
+  return n < 0 ? 0 : prm.M;
+}
+
+__device__ __forceinline__ float4 load4(const float* p) { return *reinterpret_cast<const float4*>(p); }
+__device__ __forceinline__ float4 load4(const __nv_bfloat16* p) {
+  const uint2 u = *reinterpret_cast<const uint2*>(p);
+  return make_float4(__uint_as_float(u.x << 16), __uint_as_float(u.x & 0xFFFF0000u),
+                     __uint_as_float(u.y << 16), __uint_as_float(u.y & 0xFFFF0000u));
+}
+__device__ __forceinline__ void store4(float* p, float4 v) { *reinterpret_cast<float4*>(p) = v; }
+__device__ __forceinline__ void store4(__nv_bfloat16* p, float4 v) {
+  *reinterpret_cast<uint2*>(p) = make_uint2(pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w));
+}
+
+}  // namespace pa

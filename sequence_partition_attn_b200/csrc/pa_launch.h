@@ -33,4 +33,16 @@ int launch_reduce_pair(const ReducePairParams& prm, cudaStream_t st);
 int launch_relayout(const void* src, void* dst, long long n0, long long n1, long long dst_n0, int dst_N,
                     int H, int row_bytes, int sm_count, cudaStream_t st);
 
+// delta[row] = dout[row] . o[row] - dlse[row] (dlse may be null).
+int launch_delta(const void* o, const void* dout, const float* dlse, float* delta, long long rows, int D, int dtype,
+                 cudaStream_t st);
+int attn_bwd_fma_tile_rows();
+int launch_attn_bwd_fma(const BwdParams& prm, int dtype, cudaStream_t st);
+
+int launch_cache_store(const CacheStoreParams& prm, unsigned blocks, int dtype, int D, cudaStream_t st);
+
+int cache_attn_fma_tile_rows();
+int launch_cache_attn_fma(const CacheAttnParams& prm, int dtype, cudaStream_t st);
+int launch_cache_join(const CacheAttnParams& prm, int dtype, cudaStream_t st);
+
 }  // namespace pa
