@@ -63,8 +63,8 @@ struct Smem {
 
 // Rows [r0, r0 + 64) of a [.., D] tensor into shared memory; rows at or past `end` read as 0,
 // so that nothing outside the range (which may be non-finite) reaches a product.
-template <typename T, int D>
-__device__ __forceinline__ void load_tile(float* dst, const T* src, int r0, int end) {
+template <int D>
+__device__ __forceinline__ void load_tile(float* dst, const float* src, int r0, int end) {
   for (int i = threadIdx.x; i < kT * D / 4; i += kThreads) {
     const int r = i / (D / 4), c = (i % (D / 4)) * 4;
     const float4 v = r0 + r < end ? load4(src + static_cast<size_t>(r0 + r) * D + c) : make_float4(0.f, 0.f, 0.f, 0.f);
@@ -122,7 +122,7 @@ __device__ __forceinline__ void add_product(float (&acc)[4][D / 16], const float
 // kDq: the block owns 64 query rows and streams keys; else it owns 64 keys and streams queries.
 // Four rows by four keys per thread: 8 shared 16-byte reads per 64 multiply-adds, which is what
 // bounds it (shared memory reads at twice the rate the FMA pipe would need).
-template <typename T, int D, bool kDq>
+template <int D, bool kDq>
 __global__ void __launch_bounds__(kThreads) attn_bwd_fma_kernel(const __grid_constant__ BwdParams prm) {
   extern __shared__ __align__(16) float smem[];
   float* sQ = smem;
@@ -141,10 +141,10 @@ __global__ void __launch_bounds__(kThreads) attn_bwd_fma_kernel(const __grid_con
   const int own0 = t.qg_row0[g] + (blockIdx.x - t.tile_start[g]) * kT;
   const int own1 = min(own0 + kT, t.qg_row0[g + 1]);
   const size_t head = static_cast<size_t>(bh) * prm.N;
-  const T* q = static_cast<const T*>(prm.q) + head * D;
-  const T* k = static_cast<const T*>(prm.k) + head * D;
-  const T* v = static_cast<const T*>(prm.v) + head * D;
-  const T* dout = static_cast<const T*>(prm.dout) + head * D;
+  const float* q = static_cast<const float*>(prm.q) + head * D;
+  const float* k = static_cast<const float*>(prm.k) + head * D;
+  const float* v = static_cast<const float*>(prm.v) + head * D;
+  const float* dout = static_cast<const float*>(prm.dout) + head * D;
 
   float acc0[4][D / 16] = {}, acc1[4][D / 16] = {};      // dQ | dK, dV
   for (int p = 0; p < t.P;) {
@@ -154,10 +154,10 @@ __global__ void __launch_bounds__(kThreads) attn_bwd_fma_kernel(const __grid_con
       const int q0 = kDq ? own0 : st0, q1 = kDq ? own1 : s1;
       const int k0 = kDq ? st0 : own0, k1 = kDq ? s1 : own1;
       __syncthreads();
-      load_tile<T, D>(sQ, q, q0, q1);
-      load_tile<T, D>(sdO, dout, q0, q1);
-      load_tile<T, D>(sK, k, k0, k1);
-      load_tile<T, D>(sV, v, k0, k1);
+      load_tile<D>(sQ, q, q0, q1);
+      load_tile<D>(sdO, dout, q0, q1);
+      load_tile<D>(sK, k, k0, k1);
+      load_tile<D>(sV, v, k0, k1);
       if (threadIdx.x < kT) {
         const int r = q0 + threadIdx.x;
         // +inf makes every P of the row 0: rows outside the range, and rows without any key
@@ -193,8 +193,8 @@ __global__ void __launch_bounds__(kThreads) attn_bwd_fma_kernel(const __grid_con
       }
     }
   }
-  T* out0 = static_cast<T*>(kDq ? prm.dq : prm.dk) + head * D;
-  T* out1 = static_cast<T*>(prm.dv) + head * D;
+  float* out0 = static_cast<float*>(kDq ? prm.dq : prm.dk) + head * D;
+  float* out1 = static_cast<float*>(prm.dv) + head * D;
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const int r = own0 + 4 * ty + i;
@@ -210,15 +210,15 @@ __global__ void __launch_bounds__(kThreads) attn_bwd_fma_kernel(const __grid_con
   }
 }
 
-template <typename T, int D>
+template <int D>
 int fma_impl(const BwdParams& prm, cudaStream_t st) {
   constexpr int smem = Smem<D>::kBytes;
-  cudaError_t e = cudaFuncSetAttribute(attn_bwd_fma_kernel<T, D, false>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  cudaError_t e = cudaFuncSetAttribute(attn_bwd_fma_kernel<D, false>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e == cudaSuccess)
-    e = cudaFuncSetAttribute(attn_bwd_fma_kernel<T, D, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    e = cudaFuncSetAttribute(attn_bwd_fma_kernel<D, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return static_cast<int>(e);
-  attn_bwd_fma_kernel<T, D, false><<<dim3(prm.tiles_k, prm.BH), kThreads, smem, st>>>(prm);
-  attn_bwd_fma_kernel<T, D, true><<<dim3(prm.tiles_q, prm.BH), kThreads, smem, st>>>(prm);
+  attn_bwd_fma_kernel<D, false><<<dim3(prm.tiles_k, prm.BH), kThreads, smem, st>>>(prm);
+  attn_bwd_fma_kernel<D, true><<<dim3(prm.tiles_q, prm.BH), kThreads, smem, st>>>(prm);
   return static_cast<int>(cudaGetLastError());
 }
 
@@ -243,9 +243,8 @@ int launch_delta(const void* o, const void* dout, const float* dlse, float* delt
                  : delta_impl<float, 128>(o, dout, dlse, delta, rows, st);
 }
 
-int launch_attn_bwd_fma(const BwdParams& prm, int dtype, cudaStream_t st) {
-  if (dtype == PA_BF16) return prm.D == 64 ? fma_impl<__nv_bfloat16, 64>(prm, st) : fma_impl<__nv_bfloat16, 128>(prm, st);
-  return prm.D == 64 ? fma_impl<float, 64>(prm, st) : fma_impl<float, 128>(prm, st);
+int launch_attn_bwd_fma(const BwdParams& prm, cudaStream_t st) {
+  return prm.D == 64 ? fma_impl<64>(prm, st) : fma_impl<128>(prm, st);
 }
 
 }  // namespace pa

@@ -1,0 +1,540 @@
+// attn_bwd_tc.cu -- bf16 backward pass of attention with reuse on sm_100a tensor cores
+// (tcgen05 + TMEM + TMA).  The mathematics is at the top of attn_bwd.cu.
+//
+// Two kernels, each owning a 128-row tile and streaming 128-row tiles of the other side over the
+// fresh ranges of its group (neighbouring partitions join: the gradient needs no partition
+// states).  No atomics: a tile's sums belong to one CTA, in a fixed order.
+//
+//   dK, dV  owns K, V; streams Q, dO.   S^T = K Q^T, dP^T = V dO^T (TMEM lanes are keys),
+//           dV += P^T dO, dK += dS^T Q.  4 products of 128 x 128 x D.
+//   dQ      owns Q, dO; streams K, V.   S = Q K^T, dP = dO V^T (lanes are queries),
+//           dQ += dS K.  3 products.
+// P and dS are rounded to bf16 for the second products, as the forward pass rounds P; they are
+// written to TMEM over the scores they come from and read from there (A operand in TMEM), so
+// neither goes through shared memory.
+//
+// Roles (384 threads, one CTA per SM).  warp 0: TMA producer.  warp 1: TMEM owner and MMA issuer
+// (whole warp, one elected lane issues; it also zeroes the rows behind a range shorter than a
+// tile).  warp 3 (dK, dV): -LSE and -delta of the streamed queries into shared memory.  warps
+// 4-7 and 8-11: two warpgroups, one TMEM lane per thread, columns 0-63 and 64-127 of the scores.
+// Launched at 168 registers: warpgroup 0 drops to 88, the others rise to 208.
+//
+// Ordering.  tcgen05 products of one thread run in issue order and a commit tracks all earlier
+// ones, so a product may overwrite columns that an earlier issued one reads.
+#include "mma_tiles.cuh"
+#include "pa_launch.h"
+
+namespace pa {
+namespace {
+
+using namespace tiles;
+
+constexpr int kThreads = 384;
+constexpr int kRegsLow = 88, kRegsHigh = 208;
+static_assert(kRegsLow + 2 * kRegsHigh == 3 * 168, "register split must equal the launch allocation");
+constexpr int kStages = 2;
+constexpr float kLog2e = 1.4426950408889634f;
+
+// 64 packed weights -> 32 TMEM columns.
+__device__ __forceinline__ void store_weights(uint32_t tmem, const uint32_t (&w)[32]) {
+  tmem_st32(tmem, w);
+  tmem_wait_st();
+  tc_fence_before();
+}
+
+__device__ __forceinline__ void read_scores(uint32_t tmem, float (&s)[64]) {
+  uint32_t r[64];
+  tmem_ld64(tmem, r);
+  tmem_wait_ld();
+#pragma unroll
+  for (int i = 0; i < 64; ++i) s[i] = __uint_as_float(r[i]);
+}
+
+__device__ __forceinline__ int owner_group(const AttnTables& t, int tile) {
+  int g = 0;
+  while (g + 1 < t.QG && t.tile_start[g + 1] <= tile) ++g;
+  return g;
+}
+
+// ------------------------------------------------------------------ dK, dV
+template <int D>
+struct KvLayout {
+  static constexpr int kTile = tile_bytes<D>();
+  static constexpr int kK = 0, kV = kTile;
+  static constexpr int kQ = 2 * kTile;                        // [stage]
+  static constexpr int kO = kQ + kStages * kTile;             // dO [stage]
+  static constexpr int kStat = kO + kStages * kTile;          // [slot]{-LSE log2e [128], -delta [128]}
+  static constexpr int kBar = kStat + 2 * 2 * kRows * 4;
+  enum { KV_FULL = 0, Q_FULL = 1, O_FULL = Q_FULL + kStages, Q_EMPTY = O_FULL + kStages,
+         O_EMPTY = Q_EMPTY + kStages, STAT_FULL = O_EMPTY + kStages, STAT_EMPTY = STAT_FULL + 2,
+         S_FULL = STAT_EMPTY + 2, DP_FULL, P_FULL, DS_FULL, FINAL, NBAR };
+  static constexpr int kSlot = kBar + NBAR * 8;
+  static constexpr int kAbort = kSlot + 8;
+  static constexpr int kBytes = kAbort + 8 + 1024;
+  static_assert(kBytes <= 227 * 1024, "shared memory budget");
+};
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1) attn_bwd_kv_kernel(const __grid_constant__ BwdTcParams prm) {
+  using L = KvLayout<D>;
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t raw = smem_u32(smem_raw);
+  const uint32_t base = (raw + 1023u) & ~1023u;
+  uint8_t* gbase = smem_raw + (base - raw);
+  auto bar = [&](int i) { return base + L::kBar + 8u * i; };
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(gbase + L::kAbort);
+  int* status = prm.status;
+  const AttnTables& t = prm.t;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int bh = blockIdx.x / prm.tiles_total;
+  const int tile = blockIdx.x - bh * prm.tiles_total;
+  const int g = owner_group(t, tile);
+  const int own0 = t.qg_row0[g] + (tile - t.tile_start[g]) * kRows;
+  const int own1 = t.qg_row0[g + 1];
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < L::NBAR; ++i) {
+      uint32_t n = 1;
+      if (i == L::STAT_FULL || i == L::STAT_FULL + 1) n = 32;
+      if (i == L::STAT_EMPTY || i == L::STAT_EMPTY + 1 || i == L::P_FULL || i == L::DS_FULL) n = 256;
+      mbar_init(bar(i), n);
+    }
+    *abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (warp == 1) {
+    tmem_alloc(base + L::kSlot, 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(gbase + L::kSlot);
+  const uint32_t tX = tmem, tY = tmem + 128, tDV = tmem + 256, tDK = tmem + 384;
+  auto sQ = [&](int s) { return base + L::kQ + s * L::kTile; };
+  auto sO = [&](int s) { return base + L::kO + s * L::kTile; };
+  const int n_tiles = count_tiles(t, g);
+
+  if (warp < 4) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsLow));
+    if (warp == 0) {
+      // ---------------------------------------------------------------- producer
+      if (lane == 0 && n_tiles > 0) {
+        mbar_expect_tx(bar(L::KV_FULL), 2 * L::kTile);
+        load_tile<D>(base + L::kK, &prm.tm_k, own0, bh, bar(L::KV_FULL));
+        load_tile<D>(base + L::kV, &prm.tm_v, own0, bh, bar(L::KV_FULL));
+        int j = 0, nq = 0, no = 0;
+        for (TileWalk w(t, g); w.valid(); w.next(), ++j) {
+          const int s = j % kStages;
+          const uint32_t ph = (j / kStages - 1) & 1;
+          if (j >= kStages && !mbar_wait(bar(L::Q_EMPTY + s), ph, abort_flag, status)) break;
+          mbar_expect_tx(bar(L::Q_FULL + s), L::kTile);
+          load_tile<D>(sQ(s), &prm.tm_q, w.row(), bh, bar(L::Q_FULL + s));
+          ++nq;
+          if (j >= kStages && !mbar_wait(bar(L::O_EMPTY + s), ph, abort_flag, status)) break;
+          mbar_expect_tx(bar(L::O_FULL + s), L::kTile);
+          load_tile<D>(sO(s), &prm.tm_do, w.row(), bh, bar(L::O_FULL + s));
+          ++no;
+        }
+        // every load issued lands before the CTA exits
+        mbar_drain(bar(L::KV_FULL), 0);
+        for (int i = max(0, nq - kStages); i < nq; ++i) mbar_drain(bar(L::Q_FULL + i % kStages), (i / kStages) & 1);
+        for (int i = max(0, no - kStages); i < no; ++i) mbar_drain(bar(L::O_FULL + i % kStages), (i / kStages) & 1);
+      }
+    } else if (warp == 1) {
+      // ---------------------------------------------------------------- MMA issuer
+      if (n_tiles > 0) {
+        const uint64_t aK = kmajor(base + L::kK), aV = kmajor(base + L::kV);
+        auto wait = [&](int b, uint32_t parity) { return mbar_wait_warp(bar(b), parity, abort_flag, status); };
+        auto commit = [&](int b) {
+          if (elect_one()) mma_commit(bar(b));
+          __syncwarp();
+        };
+        TileWalk w(t, g);
+        // the operands of tile j are in shared memory, and zero behind a short range
+        auto ready = [&](int j) {
+          const int s = j % kStages;
+          const uint32_t ph = (j / kStages) & 1;
+          if (!wait(L::Q_FULL + s, ph) || !wait(L::O_FULL + s, ph)) return false;
+          if (w.is_short()) {
+            zero_rows<D>(gbase + L::kQ + s * L::kTile, w.last(), lane);
+            zero_rows<D>(gbase + L::kO + s * L::kTile, w.last(), lane);
+          }
+          w.next();
+          tc_fence_after();
+          return true;
+        };
+        bool ok = wait(L::KV_FULL, 0) && ready(0);
+        int done = 0;                    // tiles whose Q_EMPTY, O_EMPTY commits were issued
+        if (ok) {
+          product_nt<D>(tX, aK, kmajor(sQ(0)));
+          commit(L::S_FULL);
+          product_nt<D>(tY, aV, kmajor(sO(0)));
+          commit(L::DP_FULL);
+        }
+        for (int j = 0; ok && j < n_tiles; ++j) {
+          const int s = j % kStages, s1 = (j + 1) % kStages;
+          const bool more = j + 1 < n_tiles;
+          if (more && !(ok = ready(j + 1))) break;
+          if (!(ok = wait(L::P_FULL, j & 1))) break;
+          tc_fence_after();
+          product_w<D>(tDV, tX, mnmajor(sO(s)), j == 0);
+          commit(L::O_EMPTY + s);
+          if (more) {
+            product_nt<D>(tX, aK, kmajor(sQ(s1)));
+            commit(L::S_FULL);
+          }
+          if (!(ok = wait(L::DS_FULL, j & 1))) break;
+          tc_fence_after();
+          product_w<D>(tDK, tY, mnmajor(sQ(s)), j == 0);
+          commit(L::Q_EMPTY + s);
+          ++done;
+          if (more) {
+            product_nt<D>(tY, aV, kmajor(sO(s1)));
+            commit(L::DP_FULL);
+          } else {
+            commit(L::FINAL);
+          }
+        }
+        if (lane == 0)                   // the last commits arrive before the CTA exits
+          for (int i = max(0, done - kStages); i < done; ++i) {
+            mbar_drain(bar(L::O_EMPTY + i % kStages), (i / kStages) & 1);
+            mbar_drain(bar(L::Q_EMPTY + i % kStages), (i / kStages) & 1);
+          }
+      }
+    } else if (warp == 3) {
+      // ---------------------------------------------------------------- LSE and delta
+      const size_t head = static_cast<size_t>(bh) * prm.N;
+      int j = 0;
+      for (TileWalk w(t, g); w.valid(); w.next(), ++j) {
+        const int s = j & 1;
+        float nl[4], nd[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int c = lane * 4 + i;
+          const bool in = c >= w.first() && c < w.last();
+          const float l = in ? prm.lse[head + w.row() + c] : -INFINITY;
+          // exp2(s + -inf) = 0: columns outside the tile's rows, and rows without any key
+          nl[i] = l == -INFINITY ? -INFINITY : -l * kLog2e;
+          nd[i] = in ? -prm.delta[head + w.row() + c] : 0.0f;
+        }
+        if (j >= 2 && !mbar_wait_warp(bar(L::STAT_EMPTY + s), (j / 2 - 1) & 1, abort_flag, status)) break;
+        float* stat = reinterpret_cast<float*>(gbase + L::kStat) + s * 2 * kRows;
+        *reinterpret_cast<float4*>(stat + lane * 4) = make_float4(nl[0], nl[1], nl[2], nl[3]);
+        *reinterpret_cast<float4*>(stat + kRows + lane * 4) = make_float4(nd[0], nd[1], nd[2], nd[3]);
+        mbar_arrive(bar(L::STAT_FULL + s));
+      }
+    }
+  } else {
+    // ---------------------------------------------------------------- P and dS, then the stores
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsHigh));
+    const int x = (warp - 4) >> 2;                    // columns 64 x .. 64 x + 63
+    const int row = (warp & 3) * 32 + lane;
+    const uint32_t lane_off = static_cast<uint32_t>((warp & 3) * 32) << 16;
+    const uint32_t sX = tX + lane_off + x * 64, sY = tY + lane_off + x * 64;
+    const float2 scale2 = make_float2(prm.scale_log2, prm.scale_log2);
+    bool ok = true;
+    for (int j = 0; j < n_tiles; ++j) {
+      const int slot = j & 1;
+      const float4* nl = reinterpret_cast<const float4*>(gbase + L::kStat + (slot * 2 * kRows + x * 64) * 4);
+      const float4* nd = nl + kRows / 4;
+      if (!mbar_wait(bar(L::STAT_FULL + slot), (j / 2) & 1, abort_flag, status) ||
+          !mbar_wait(bar(L::S_FULL), j & 1, abort_flag, status)) {
+        ok = false;
+        break;
+      }
+      tc_fence_after();
+      float p[64];
+      read_scores(sX, p);
+      uint32_t w[32];
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        const float4 l = nl[i];
+        const float2 a = __ffma2_rn(make_float2(p[4 * i], p[4 * i + 1]), scale2, make_float2(l.x, l.y));
+        const float2 b = __ffma2_rn(make_float2(p[4 * i + 2], p[4 * i + 3]), scale2, make_float2(l.z, l.w));
+        p[4 * i] = fast_exp2(a.x);
+        p[4 * i + 1] = fast_exp2(a.y);
+        p[4 * i + 2] = fast_exp2(b.x);
+        p[4 * i + 3] = fast_exp2(b.y);
+        w[2 * i] = pack_bf16x2(p[4 * i], p[4 * i + 1]);
+        w[2 * i + 1] = pack_bf16x2(p[4 * i + 2], p[4 * i + 3]);
+      }
+      store_weights(sX, w);
+      mbar_arrive(bar(L::P_FULL));
+      if (!mbar_wait(bar(L::DP_FULL), j & 1, abort_flag, status)) {
+        ok = false;
+        break;
+      }
+      tc_fence_after();
+      float dp[64];
+      read_scores(sY, dp);
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        const float4 d = nd[i];
+        const float2 a = __fmul2_rn(make_float2(p[4 * i], p[4 * i + 1]),
+                                    __fadd2_rn(make_float2(dp[4 * i], dp[4 * i + 1]), make_float2(d.x, d.y)));
+        const float2 b = __fmul2_rn(make_float2(p[4 * i + 2], p[4 * i + 3]),
+                                    __fadd2_rn(make_float2(dp[4 * i + 2], dp[4 * i + 3]), make_float2(d.z, d.w)));
+        w[2 * i] = pack_bf16x2(a.x, a.y);
+        w[2 * i + 1] = pack_bf16x2(b.x, b.y);
+      }
+      store_weights(sY, w);
+      mbar_arrive(bar(L::DS_FULL));
+      mbar_arrive(bar(L::STAT_EMPTY + slot));
+    }
+    // warpgroup 0 stores dV, warpgroup 1 dK
+    __nv_bfloat16* out = static_cast<__nv_bfloat16*>(x ? prm.out0 : prm.out1) +
+                         (static_cast<size_t>(bh) * prm.N + own0 + row) * D;
+    const bool row_ok = own0 + row < own1;
+    if (n_tiles == 0) {
+      if (row_ok)
+        for (int c = 0; c < D / 8; ++c) reinterpret_cast<uint4*>(out)[c] = make_uint4(0, 0, 0, 0);
+    } else if (ok && mbar_wait(bar(L::FINAL), 0, abort_flag, status)) {
+      tc_fence_after();
+      store_rows<D>((x ? tDK : tDV) + lane_off, out, x ? prm.scale : 1.0f, row_ok);
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+// ------------------------------------------------------------------ dQ
+// Scores rotate through three TMEM regions so that S of the next tile is there when the threads
+// turn to it: S(j) in R[2j % 3], dP(j) in R[(2j + 1) % 3] (dS(j) over it), S(j + 1) in the third.
+// dP(j + 1) goes where S(j) was, once it has been read; S(j + 2) where dS(j) was, after dQ(j).
+// S(j + 1) and dP(j + 1) are issued before the threads are done with tile j, so every barrier
+// between the issuer and the threads comes in two, by the tile's parity: a waiter can be at most
+// one phase behind on each.
+constexpr int kKStages = 3, kVStages = 2;     // K(j) is held until dQ(j), V(j) only until dP(j)
+
+template <int D>
+struct QLayout {
+  static constexpr int kTile = tile_bytes<D>();
+  static constexpr int kQ = 0, kO = kTile;
+  static constexpr int kK = 2 * kTile;                        // [stage]
+  static constexpr int kV = kK + kKStages * kTile;            // [stage]
+  static constexpr int kBar = kV + kVStages * kTile;
+  enum { OWN_FULL = 0, K_FULL = 1, V_FULL = K_FULL + kKStages, K_EMPTY = V_FULL + kVStages,
+         V_EMPTY = K_EMPTY + kKStages, S_FULL = V_EMPTY + kVStages,
+         DP_FULL = S_FULL + 2, S_READ = DP_FULL + 2, DS_FULL = S_READ + 2, FINAL = DS_FULL + 2, NBAR };
+  static constexpr int kSlot = kBar + NBAR * 8;
+  static constexpr int kAbort = kSlot + 8;
+  static constexpr int kBytes = kAbort + 8 + 1024;
+  static_assert(kBytes <= 227 * 1024, "shared memory budget");
+};
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1) attn_bwd_q_kernel(const __grid_constant__ BwdTcParams prm) {
+  using L = QLayout<D>;
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t raw = smem_u32(smem_raw);
+  const uint32_t base = (raw + 1023u) & ~1023u;
+  uint8_t* gbase = smem_raw + (base - raw);
+  auto bar = [&](int i) { return base + L::kBar + 8u * i; };
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(gbase + L::kAbort);
+  int* status = prm.status;
+  const AttnTables& t = prm.t;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int bh = blockIdx.x / prm.tiles_total;
+  const int tile = blockIdx.x - bh * prm.tiles_total;
+  const int g = owner_group(t, tile);
+  const int own0 = t.qg_row0[g] + (tile - t.tile_start[g]) * kRows;
+  const int own1 = t.qg_row0[g + 1];
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < L::NBAR; ++i)
+      mbar_init(bar(i), i >= L::S_READ && i < L::FINAL ? 256u : 1u);
+    *abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (warp == 1) {
+    tmem_alloc(base + L::kSlot, 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(gbase + L::kSlot);
+  const uint32_t tDQ = tmem + 384;
+  auto region = [&](int i) { return tmem + 128u * (i % 3); };
+  auto sK = [&](int j) { return base + L::kK + (j % kKStages) * L::kTile; };
+  auto sV = [&](int j) { return base + L::kV + (j % kVStages) * L::kTile; };
+  const int n_tiles = count_tiles(t, g);
+
+  if (warp < 4) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsLow));
+    if (warp == 0) {
+      // ---------------------------------------------------------------- producer
+      if (lane == 0 && n_tiles > 0) {
+        mbar_expect_tx(bar(L::OWN_FULL), 2 * L::kTile);
+        load_tile<D>(base + L::kQ, &prm.tm_q, own0, bh, bar(L::OWN_FULL));
+        load_tile<D>(base + L::kO, &prm.tm_do, own0, bh, bar(L::OWN_FULL));
+        int j = 0, nk = 0, nv = 0;
+        for (TileWalk w(t, g); w.valid(); w.next(), ++j) {
+          const int s = j % kKStages, u = j % kVStages;
+          if (j >= kKStages && !mbar_wait(bar(L::K_EMPTY + s), (j / kKStages - 1) & 1, abort_flag, status)) break;
+          mbar_expect_tx(bar(L::K_FULL + s), L::kTile);
+          load_tile<D>(sK(j), &prm.tm_k, w.row(), bh, bar(L::K_FULL + s));
+          ++nk;
+          if (j >= kVStages && !mbar_wait(bar(L::V_EMPTY + u), (j / kVStages - 1) & 1, abort_flag, status)) break;
+          mbar_expect_tx(bar(L::V_FULL + u), L::kTile);
+          load_tile<D>(sV(j), &prm.tm_v, w.row(), bh, bar(L::V_FULL + u));
+          ++nv;
+        }
+        mbar_drain(bar(L::OWN_FULL), 0);
+        for (int i = max(0, nk - kKStages); i < nk; ++i) mbar_drain(bar(L::K_FULL + i % kKStages), (i / kKStages) & 1);
+        for (int i = max(0, nv - kVStages); i < nv; ++i) mbar_drain(bar(L::V_FULL + i % kVStages), (i / kVStages) & 1);
+      }
+    } else if (warp == 1) {
+      // ---------------------------------------------------------------- MMA issuer
+      if (n_tiles > 0) {
+        const uint64_t aQ = kmajor(base + L::kQ), aO = kmajor(base + L::kO);
+        auto wait = [&](int b, uint32_t parity) { return mbar_wait_warp(bar(b), parity, abort_flag, status); };
+        auto commit = [&](int b) {
+          if (elect_one()) mma_commit(bar(b));
+          __syncwarp();
+        };
+        TileWalk wk(t, g), wv(t, g);
+        // K(j), V(j) in shared memory, and zero behind a short range
+        auto issue_s = [&](int j) {
+          if (!wait(L::K_FULL + j % kKStages, (j / kKStages) & 1)) return false;
+          if (wk.is_short()) zero_rows<D>(gbase + (sK(j) - base), wk.last(), lane);
+          wk.next();
+          tc_fence_after();
+          product_nt<D>(region(2 * j), aQ, kmajor(sK(j)));
+          commit(L::S_FULL + (j & 1));
+          return true;
+        };
+        auto issue_dp = [&](int j) {
+          if (!wait(L::V_FULL + j % kVStages, (j / kVStages) & 1)) return false;
+          if (wv.is_short()) zero_rows<D>(gbase + (sV(j) - base), wv.last(), lane);
+          wv.next();
+          tc_fence_after();
+          product_nt<D>(region(2 * j + 1), aO, kmajor(sV(j)));
+          commit(L::V_EMPTY + j % kVStages);
+          commit(L::DP_FULL + (j & 1));
+          return true;
+        };
+        bool ok = wait(L::OWN_FULL, 0) && issue_s(0) && issue_dp(0) && (n_tiles < 2 || issue_s(1));
+        int done = 0;
+        for (int j = 0; ok && j < n_tiles; ++j) {
+          if (j + 1 < n_tiles && !(ok = wait(L::S_READ + (j & 1), (j / 2) & 1) && issue_dp(j + 1))) break;
+          if (!(ok = wait(L::DS_FULL + (j & 1), (j / 2) & 1))) break;
+          tc_fence_after();
+          product_w<D>(tDQ, region(2 * j + 1), mnmajor(sK(j)), j == 0);
+          commit(L::K_EMPTY + j % kKStages);
+          ++done;
+          if (j + 1 == n_tiles) commit(L::FINAL);
+          if (j + 2 < n_tiles) ok = issue_s(j + 2);
+        }
+        if (lane == 0)
+          for (int i = max(0, done - kKStages); i < done; ++i)
+            mbar_drain(bar(L::K_EMPTY + i % kKStages), (i / kKStages) & 1);
+      }
+    }
+  } else {
+    // ---------------------------------------------------------------- dS, then the store
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsHigh));
+    const int x = (warp - 4) >> 2;
+    const int row = (warp & 3) * 32 + lane;
+    const uint32_t lane_off = (static_cast<uint32_t>((warp & 3) * 32) << 16) + x * 64;
+    const bool row_ok = own0 + row < own1;
+    const size_t at = static_cast<size_t>(bh) * prm.N + own0 + row;
+    const float l = row_ok ? prm.lse[at] : -INFINITY;
+    const float nl = l == -INFINITY ? -INFINITY : -l * kLog2e;    // no key: every P is 0
+    const float nd = row_ok ? -prm.delta[at] : 0.0f;
+    const float2 scale2 = make_float2(prm.scale_log2, prm.scale_log2);
+    const float2 nl2 = make_float2(nl, nl), nd2 = make_float2(nd, nd);
+    bool ok = true;
+    TileWalk w(t, g);
+    for (int j = 0; j < n_tiles; ++j, w.next()) {
+      if (!mbar_wait(bar(L::S_FULL + (j & 1)), (j / 2) & 1, abort_flag, status)) {
+        ok = false;
+        break;
+      }
+      tc_fence_after();
+      float p[64];
+      read_scores(region(2 * j) + lane_off, p);
+      tc_fence_before();
+      mbar_arrive(bar(L::S_READ + (j & 1)));
+      if (w.first() > 0 || w.last() < kRows) {
+#pragma unroll
+        for (int c = 0; c < 64; ++c)
+          if (x * 64 + c < w.first() || x * 64 + c >= w.last()) p[c] = -INFINITY;
+      }
+#pragma unroll
+      for (int i = 0; i < 32; ++i) {
+        const float2 a = __ffma2_rn(make_float2(p[2 * i], p[2 * i + 1]), scale2, nl2);
+        p[2 * i] = fast_exp2(a.x);
+        p[2 * i + 1] = fast_exp2(a.y);
+      }
+      if (!mbar_wait(bar(L::DP_FULL + (j & 1)), (j / 2) & 1, abort_flag, status)) {
+        ok = false;
+        break;
+      }
+      tc_fence_after();
+      float dp[64];
+      read_scores(region(2 * j + 1) + lane_off, dp);
+      uint32_t ds[32];
+#pragma unroll
+      for (int i = 0; i < 32; ++i) {
+        const float2 a = __fmul2_rn(make_float2(p[2 * i], p[2 * i + 1]),
+                                    __fadd2_rn(make_float2(dp[2 * i], dp[2 * i + 1]), nd2));
+        ds[i] = pack_bf16x2(a.x, a.y);
+      }
+      store_weights(region(2 * j + 1) + lane_off, ds);
+      mbar_arrive(bar(L::DS_FULL + (j & 1)));
+    }
+    // each warpgroup stores half of dQ's columns
+    __nv_bfloat16* out = static_cast<__nv_bfloat16*>(prm.out0) + at * D + x * (D / 2);
+    if (n_tiles == 0) {
+      if (row_ok)
+        for (int c = 0; c < D / 16; ++c) reinterpret_cast<uint4*>(out)[c] = make_uint4(0, 0, 0, 0);
+    } else if (ok && mbar_wait(bar(L::FINAL), 0, abort_flag, status)) {
+      tc_fence_after();
+      store_rows<D / 2>(tDQ + (lane_off & 0xFFFF0000u) + x * (D / 2), out, prm.scale, row_ok);
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+template <int D>
+int kv_impl(const BwdTcParams& prm, int units, cudaStream_t st) {
+  cudaError_t e = cudaFuncSetAttribute(attn_bwd_kv_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, KvLayout<D>::kBytes);
+  if (e != cudaSuccess) return static_cast<int>(e);
+  attn_bwd_kv_kernel<D><<<units, kThreads, KvLayout<D>::kBytes, st>>>(prm);
+  return static_cast<int>(cudaGetLastError());
+}
+
+template <int D>
+int q_impl(const BwdTcParams& prm, int units, cudaStream_t st) {
+  cudaError_t e = cudaFuncSetAttribute(attn_bwd_q_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, QLayout<D>::kBytes);
+  if (e != cudaSuccess) return static_cast<int>(e);
+  attn_bwd_q_kernel<D><<<units, kThreads, QLayout<D>::kBytes, st>>>(prm);
+  return static_cast<int>(cudaGetLastError());
+}
+
+}  // namespace
+
+int attn_bwd_tc_tile_rows() { return kRows; }
+
+int launch_attn_bwd_kv(const BwdTcParams& prm, int D, int units, cudaStream_t st) {
+  return D == 64 ? kv_impl<64>(prm, units, st) : kv_impl<128>(prm, units, st);
+}
+
+int launch_attn_bwd_q(const BwdTcParams& prm, int D, int units, cudaStream_t st) {
+  return D == 64 ? q_impl<64>(prm, units, st) : q_impl<128>(prm, units, st);
+}
+
+}  // namespace pa

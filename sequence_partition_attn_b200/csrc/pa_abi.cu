@@ -726,15 +726,45 @@ static int pa_attn_backward_impl(pa_ctx* ctx, const pa_attn_bwd_desc* d, void* s
   prm.N = d->N;
   prm.D = d->D;
   prm.scale = d->scale;
-  const int tile = pa::attn_bwd_fma_tile_rows();
-  prm.tiles_q = fill_owner_tiles(prm.tq, tile);
-  prm.tiles_k = fill_owner_tiles(prm.tk, tile);
   const long long rows = BH * d->N;
   if (rows > 0x7fffffffLL * 8) return fail(ctx, PA_EINVAL, "too many rows");
+  const int tile = d->dtype == PA_BF16 ? pa::attn_bwd_tc_tile_rows() : pa::attn_bwd_fma_tile_rows();
+  prm.tiles_q = fill_owner_tiles(prm.tq, tile);
+  prm.tiles_k = fill_owner_tiles(prm.tk, tile);
+  const long long units = BH * std::max(prm.tiles_q, prm.tiles_k);
+  if (units > 0x7fffffffLL) return fail(ctx, PA_EINVAL, "too many work units");
+  pa::BwdTcParams tc;
+  if (d->dtype == PA_BF16) {
+    memset(&tc, 0, sizeof tc);
+    if ((rc = encode_qkv_map(ctx, &tc.tm_q, d->q, (int)BH, d->N, d->D))) return rc;
+    if ((rc = encode_qkv_map(ctx, &tc.tm_k, d->k, (int)BH, d->N, d->D))) return rc;
+    if ((rc = encode_qkv_map(ctx, &tc.tm_v, d->v, (int)BH, d->N, d->D))) return rc;
+    if ((rc = encode_qkv_map(ctx, &tc.tm_do, d->dout, (int)BH, d->N, d->D))) return rc;
+  }
   int e = pa::launch_delta(d->o, d->dout, d->dlse, d->delta, rows, d->D, d->dtype, st);
   if (e) return cuda_fail(ctx, e, "delta launch");
-  e = pa::launch_attn_bwd_fma(prm, d->dtype, st);
-  return e ? cuda_fail(ctx, e, "attention backward launch") : PA_OK;
+  if (d->dtype == PA_F32) {
+    e = pa::launch_attn_bwd_fma(prm, st);
+    return e ? cuda_fail(ctx, e, "attention backward launch") : PA_OK;
+  }
+  tc.lse = d->lse;
+  tc.delta = d->delta;
+  tc.status = ctx->d_status;
+  tc.N = d->N;
+  tc.scale = d->scale;
+  tc.scale_log2 = d->scale * 1.4426950408889634f;
+  tc.t = prm.tk;
+  tc.tiles_total = prm.tiles_k;
+  tc.out0 = d->dk;
+  tc.out1 = d->dv;
+  e = pa::launch_attn_bwd_kv(tc, d->D, static_cast<int>(BH * prm.tiles_k), st);
+  if (e) return cuda_fail(ctx, e, "attention backward (dK, dV) launch");
+  tc.t = prm.tq;
+  tc.tiles_total = prm.tiles_q;
+  tc.out0 = d->dq;
+  tc.out1 = nullptr;
+  e = pa::launch_attn_bwd_q(tc, d->D, static_cast<int>(BH * prm.tiles_q), st);
+  return e ? cuda_fail(ctx, e, "attention backward (dQ) launch") : PA_OK;
 }
 
 static int pa_cache_store_impl(pa_ctx* ctx, const pa_cache_store_desc* d, void* stream) {

@@ -381,6 +381,19 @@ struct BwdParams {
   AttnTables tq, tk;
 };
 
+// One of the two bf16 kernels: t holds its owner groups and the partitions they stream.
+struct BwdTcParams {
+  CUtensorMap tm_q, tm_k, tm_v, tm_do;
+  const float* lse;
+  const float* delta;
+  void* out0;                     // dK | dQ
+  void* out1;                     // dV
+  int* status;
+  int N, tiles_total;
+  float scale, scale_log2;
+  AttnTables t;
+};
+
 struct CacheStoreParams {
   const void* k;                  // [B][Hk][T][D]
   const void* v;

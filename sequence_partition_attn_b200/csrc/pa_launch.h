@@ -37,7 +37,11 @@ int launch_relayout(const void* src, void* dst, long long n0, long long n1, long
 int launch_delta(const void* o, const void* dout, const float* dlse, float* delta, long long rows, int D, int dtype,
                  cudaStream_t st);
 int attn_bwd_fma_tile_rows();
-int launch_attn_bwd_fma(const BwdParams& prm, int dtype, cudaStream_t st);
+int launch_attn_bwd_fma(const BwdParams& prm, cudaStream_t st);
+
+int attn_bwd_tc_tile_rows();
+int launch_attn_bwd_kv(const BwdTcParams& prm, int D, int units, cudaStream_t st);
+int launch_attn_bwd_q(const BwdTcParams& prm, int D, int units, cudaStream_t st);
 
 int launch_cache_store(const CacheStoreParams& prm, unsigned blocks, int dtype, int D, cudaStream_t st);
 
