@@ -29,15 +29,16 @@ __device__ __forceinline__ float4 decode4(uint32_t c, float scale) {
 
 // 64 query rows per block, D / 64 threads per row (64 channels each); keys stream through
 // shared memory with an online softmax, as in the fp32 partition attention.
-template <typename T, int D>
-__global__ void __launch_bounds__(kRows * (D / 64)) cache_attn_fma_kernel(const __grid_constant__ CacheAttnParams prm) {
+template <int D>
+__global__ void __launch_bounds__(kRows * (D / 64)) cache_attn_f32_kernel(const __grid_constant__ CacheAttnParams prm) {
   constexpr int TPR = D / 64;
   __shared__ __align__(16) float sK[kKeys][D];
   __shared__ __align__(16) float sV[kKeys][D];
   const int bh = blockIdx.y;
   const int split = blockIdx.z;
   const int len = cache_len(prm, bh / prm.Hk);
-  const int k0 = split * prm.chunk, k1 = min(k0 + prm.chunk, len);
+  const int chunk = split_chunk(len, prm.splits);
+  const int k0 = min(split * chunk, len), k1 = min(k0 + chunk, len);
   const int row = blockIdx.x * kRows + threadIdx.x / TPR;
   const int half = threadIdx.x % TPR;
   const bool row_ok = row < prm.R;
@@ -48,7 +49,7 @@ __global__ void __launch_bounds__(kRows * (D / 64)) cache_attn_fma_kernel(const 
   const float* vs = prm.v_scale + static_cast<size_t>(bh) * prm.blocks;
 
   float q[64], o[64];
-  const T* qp = static_cast<const T*>(prm.q) + (row_ok ? out_row : static_cast<size_t>(bh) * prm.R) * D + half * 64;
+  const float* qp = static_cast<const float*>(prm.q) + (row_ok ? out_row : static_cast<size_t>(bh) * prm.R) * D + half * 64;
 #pragma unroll
   for (int d = 0; d < 64; d += 4) {
     const float4 v = load4(qp + d);
@@ -117,7 +118,7 @@ __global__ void __launch_bounds__(kRows * (D / 64)) cache_attn_fma_kernel(const 
     if (prm.splits > 1)
       store4(prm.ws_o + at * D + half * 64 + d, x);
     else
-      store4(static_cast<T*>(prm.o) + at * D + half * 64 + d, x);
+      store4(static_cast<float*>(prm.o) + at * D + half * 64 + d, x);
   }
   if (half == 0) (prm.splits > 1 ? prm.ws_lse : prm.lse)[at] = k1 > k0 ? m + logf(l) : -INFINITY;
 }
@@ -133,22 +134,21 @@ __global__ void __launch_bounds__(128) cache_join_kernel(const __grid_constant__
   for (int s = 0; s < prm.splits; ++s) m = fmaxf(m, prm.ws_lse[s * static_cast<size_t>(prm.rows) + row]);
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
   float sum = 0.0f;
-  if (m > -INFINITY) {
-    for (int s = 0; s < prm.splits; ++s) {
-      const size_t at = s * static_cast<size_t>(prm.rows) + row;
-      const float w = expf(prm.ws_lse[at] - m);
-      const float4 x = *reinterpret_cast<const float4*>(prm.ws_o + at * D + 4 * c);
-      sum += w;
-      acc.x = fmaf(w, x.x, acc.x);
-      acc.y = fmaf(w, x.y, acc.y);
-      acc.z = fmaf(w, x.z, acc.z);
-      acc.w = fmaf(w, x.w, acc.w);
-    }
+  for (int s = 0; s < prm.splits; ++s) {
+    const size_t at = s * static_cast<size_t>(prm.rows) + row;
+    const float lse = prm.ws_lse[at];
+    const float w = lse == -INFINITY ? 0.0f : expf(lse - m);      // a split without tokens
+    const float4 x = *reinterpret_cast<const float4*>(prm.ws_o + at * D + 4 * c);
+    sum += w;
+    acc.x = fmaf(w, x.x, acc.x);
+    acc.y = fmaf(w, x.y, acc.y);
+    acc.z = fmaf(w, x.z, acc.z);
+    acc.w = fmaf(w, x.w, acc.w);
   }
-  const float inv = sum > 0.0f ? 1.0f / sum : 0.0f;
+  const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
   acc = make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
   store4(static_cast<T*>(prm.o) + static_cast<size_t>(row) * D + 4 * c, acc);
-  if (c == 0) prm.lse[row] = sum > 0.0f ? m + logf(sum) : -INFINITY;
+  if (c == 0) prm.lse[row] = sum == 0.0f ? -INFINITY : m + logf(sum);
 }
 
 template <typename T, int D>
@@ -160,20 +160,14 @@ int join_impl(const CacheAttnParams& prm, cudaStream_t st) {
 
 }  // namespace
 
-int cache_attn_fma_tile_rows() { return kRows; }
+int cache_attn_f32_tile_rows() { return kRows; }
 
-int launch_cache_attn_fma(const CacheAttnParams& prm, int dtype, cudaStream_t st) {
+int launch_cache_attn_f32(const CacheAttnParams& prm, cudaStream_t st) {
   const dim3 grid((prm.R + kRows - 1) / kRows, prm.B * prm.Hk, prm.splits);
-  if (dtype == PA_BF16) {
-    if (prm.D == 64)
-      cache_attn_fma_kernel<__nv_bfloat16, 64><<<grid, kRows, 0, st>>>(prm);
-    else
-      cache_attn_fma_kernel<__nv_bfloat16, 128><<<grid, kRows * 2, 0, st>>>(prm);
-  } else if (prm.D == 64) {
-    cache_attn_fma_kernel<float, 64><<<grid, kRows, 0, st>>>(prm);
-  } else {
-    cache_attn_fma_kernel<float, 128><<<grid, kRows * 2, 0, st>>>(prm);
-  }
+  if (prm.D == 64)
+    cache_attn_f32_kernel<64><<<grid, kRows, 0, st>>>(prm);
+  else
+    cache_attn_f32_kernel<128><<<grid, kRows * 2, 0, st>>>(prm);
   return static_cast<int>(cudaGetLastError());
 }
 

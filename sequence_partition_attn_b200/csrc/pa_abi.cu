@@ -829,12 +829,11 @@ static int plan_cache_attn(pa_ctx* ctx, pa_dtype dtype, int B, int H, int Hk, in
   prm.D = D;
   prm.blocks = (M - 1) / PA_CACHE_BLOCK + 1;
   prm.rows = R * BHk;
-  const long long tiles = BHk * ((R + pa::cache_attn_fma_tile_rows() - 1) / pa::cache_attn_fma_tile_rows());
-  long long splits = tiles > 0 ? 4LL * ctx->sm_count / tiles : 1;
-  splits = std::max(1LL, std::min(splits, static_cast<long long>(prm.blocks) / 4));
-  const long long blocks_per = (prm.blocks + splits - 1) / splits;
-  prm.chunk = static_cast<int>(blocks_per) * PA_CACHE_BLOCK;
-  prm.splits = static_cast<int>((prm.blocks + blocks_per - 1) / blocks_per);
+  const int tile_rows = dtype == PA_BF16 ? pa::cache_attn_rows_tile_rows() : pa::cache_attn_f32_tile_rows();
+  const long long tiles = BHk * ((R + tile_rows - 1) / tile_rows);
+  // enough blocks to fill the GPU, each with at least four cache blocks of tokens
+  const long long splits = tiles > 0 ? (3LL * ctx->sm_count + tiles - 1) / tiles : 1;
+  prm.splits = static_cast<int>(std::max(1LL, std::min(splits, static_cast<long long>(prm.blocks) / 4)));
   if (prm.rows > 0x7fffffffLL) return fail(ctx, PA_EINVAL, "too many query rows");
   *ws_bytes = prm.splits > 1 ? static_cast<size_t>(prm.splits) * prm.rows * (D + 1) * sizeof(float) : 0;
   return PA_OK;
@@ -874,7 +873,7 @@ static int pa_cache_attn_impl(pa_ctx* ctx, const pa_cache_attn_desc* d, void* st
     prm.ws_lse = prm.ws_o + static_cast<size_t>(prm.splits) * prm.rows * d->D;
   }
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  int e = pa::launch_cache_attn_fma(prm, d->dtype, st);
+  int e = d->dtype == PA_BF16 ? pa::launch_cache_attn_rows(prm, st) : pa::launch_cache_attn_f32(prm, st);
   if (e) return cuda_fail(ctx, e, "cache attention launch");
   if (prm.splits > 1) e = pa::launch_cache_join(prm, d->dtype, st);
   return e ? cuda_fail(ctx, e, "cache join launch") : PA_OK;

@@ -421,7 +421,7 @@ struct CacheAttnParams {
   int* status;
   long long rows;                 // B * Hk * R
   int B, Hk, R, M, D, blocks;
-  int splits, chunk;              // tokens per split, a multiple of the cache block
+  int splits;                     // of the token axis
   float scale;
 };
 
@@ -436,6 +436,12 @@ __device__ __forceinline__ int next_range(const AttnTables& t, int g, int from, 
   while (p < t.P && (fresh_bit(t.fresh_bits, g, p) || t.part_off[p + 1] == t.part_off[p])) ++p;
   s1 = t.part_off[p];
   return p;
+}
+
+// Tokens per split of a request of `len` tokens: whole cache blocks.
+__device__ __forceinline__ int split_chunk(int len, int splits) {
+  const int blocks = (len + PA_CACHE_BLOCK - 1) / PA_CACHE_BLOCK;
+  return (blocks + splits - 1) / splits * PA_CACHE_BLOCK;
 }
 
 // Tokens held by request b's cache; a length outside [0, M] is recorded and clamped.

@@ -45,8 +45,10 @@ int launch_attn_bwd_q(const BwdTcParams& prm, int D, int units, cudaStream_t st)
 
 int launch_cache_store(const CacheStoreParams& prm, unsigned blocks, int dtype, int D, cudaStream_t st);
 
-int cache_attn_fma_tile_rows();
-int launch_cache_attn_fma(const CacheAttnParams& prm, int dtype, cudaStream_t st);
+int cache_attn_f32_tile_rows();
+int launch_cache_attn_f32(const CacheAttnParams& prm, cudaStream_t st);
+int cache_attn_rows_tile_rows();
+int launch_cache_attn_rows(const CacheAttnParams& prm, cudaStream_t st);
 int launch_cache_join(const CacheAttnParams& prm, int dtype, cudaStream_t st);
 
 }  // namespace pa
