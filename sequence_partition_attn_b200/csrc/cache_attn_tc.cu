@@ -1,0 +1,429 @@
+// cache_attn_tc.cu -- attention over the 8-bit K/V cache for many query rows per KV head (bf16
+// queries: prompts, a ring step's block) on sm_100a tensor cores.  Definition: cache_attn.cu.
+//
+// Bound by the tensor cores and the exponentials, as the bf16 partition attention (attn_tc.cu),
+// whose scheme of two 128-row query tiles per CTA it follows: S = Q K^T and O += P V on tcgen05,
+// P written to TMEM over S.  What differs is where K and V come from: a warpgroup reads the codes
+// of each 128-token tile, two cache blocks, with plain 16-byte loads (the next item's loads in
+// flight), multiplies them by the block's scale in fp32 and writes bf16 to the swizzled tile that
+// the products read.  The scale is a power of two, so code * scale is exact in bf16: nothing is
+// rounded that the cache did not round already, and the scores need no scale of their own.
+// The codes cross HBM and L2 in 8 bits; a pass that widened the cache to bf16 first would write
+// and read it again at twice the size.
+//
+// Roles (512 threads, one CTA per SM; 128 registers at launch, then 80 / 176 / 176 / 80):
+//   warp 0      loads Q_a, Q_b by TMA.     warp 1  TMEM owner and MMA issuer.
+//   warps 4..7  softmax of query tile a; warps 8..11 of tile b (one row per thread).
+//   warps 12..15 widen K and V; after the last tile they store O and LSE.
+// Rows are the (H / Hk) * Nq queries of one KV head.  A block of at most 128 rows runs tile a only.
+#include <cuda_fp8.h>
+
+#include "mma_tiles.cuh"
+#include "pa_launch.h"
+
+namespace pa {
+namespace {
+
+using tiles::kAtomBytes;
+
+constexpr int kBM = 128, kBN = 128;
+constexpr int kStages = 2;
+constexpr int kThreads = 512;
+constexpr int kRegsLow = 80, kRegsWiden = 80, kRegsHigh = 176;
+static_assert(kRegsLow + kRegsWiden + 2 * kRegsHigh == kThreads / 128 * (65536 / kThreads),
+              "register split must equal the launch allocation");
+constexpr float kLn2 = 0.6931471805599453f;
+constexpr float kRescaleLog2 = 8.0f;    // move the running max only when it grows by > 8
+
+template <int D>
+struct Layout {
+  static constexpr int kTile = tiles::tile_bytes<D>();
+  static constexpr int kQ = 0;                                 // Q_a, Q_b
+  static constexpr int kK = kQ + 2 * kTile;
+  static constexpr int kV = kK + kStages * kTile;
+  static constexpr int kML = kV + kStages * kTile;             // (max, sum) per row: [tile][row]
+  static constexpr int kBar = kML + 2 * kBM * 8;
+  enum { Q_FULL = 0, K_FULL = 1, V_FULL = K_FULL + kStages, K_EMPTY = V_FULL + kStages,
+         V_EMPTY = K_EMPTY + kStages, S_FULL = V_EMPTY + kStages, P_LO = S_FULL + 2, P_HI = P_LO + 2,
+         O_FINAL = P_HI + 2, ML_FULL = O_FINAL + 2, NBAR = ML_FULL + 2 };
+  static constexpr int kSlot = kBar + NBAR * 8;
+  static constexpr int kAbort = kSlot + 8;
+  static constexpr int kBytes = kAbort + 8 + 1024;
+  static_assert(kBytes <= 227 * 1024, "shared memory budget");
+};
+
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+
+__device__ __forceinline__ float row_max(const float (&s)[kBN]) {
+  float mx[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) mx[i] = max3(s[i], s[i + 8], s[i + 16]);
+#pragma unroll
+  for (int c = 24; c < 120; c += 16)
+#pragma unroll
+    for (int i = 0; i < 8; ++i) mx[i] = max3(mx[i], s[c + i], s[c + 8 + i]);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) mx[i] = fmaxf(mx[i], s[120 + i]);
+  return max3(max3(mx[0], mx[1], mx[2]), max3(mx[3], mx[4], mx[5]), fmaxf(mx[6], mx[7]));
+}
+
+// Weights of 64 columns: exponentials, row-sum chains, bf16 pairs (32 TMEM columns).
+template <int H>
+__device__ __forceinline__ void weights_half(const float (&s)[kBN], float m, float sl2, float2 (&acc)[4], uint32_t (&w)[32]) {
+  const float2 scale2 = make_float2(sl2, sl2), neg_m2 = make_float2(-m, -m);
+#pragma unroll
+  for (int i = 0; i < 32; ++i) {
+    const int c = H * 64 + 2 * i;
+    const float2 a = __ffma2_rn(make_float2(s[c], s[c + 1]), scale2, neg_m2);
+    const float e0 = fast_exp2(a.x), e1 = fast_exp2(a.y);
+    acc[i & 3] = __fadd2_rn(acc[i & 3], make_float2(e0, e1));
+    w[i] = pack_bf16x2(e0, e1);
+  }
+}
+
+// O_x (+)= P_x V over keys 64 H .. 64 H + 63: P's pairs are 32 consecutive TMEM columns per half.
+template <int D, int H>
+__device__ __forceinline__ void product_pv(uint32_t o_tmem, uint32_t p_tmem, uint64_t v, bool first) {
+  constexpr uint32_t id = idesc_bf16(kBM, D, false, true);
+#pragma unroll
+  for (int kk = H * 4; kk < H * 4 + 4; ++kk) {
+    if (elect_one())
+      tiles::mma_ts(o_tmem, p_tmem + kk * 8, v + static_cast<uint32_t>((kk * 16 * 128) >> 4), id,
+                    (first && kk == 0) ? 0u : 1u);
+    __syncwarp();
+  }
+}
+
+// Two codes (the low bytes) times a power of two, as a bf16 pair.
+__device__ __forceinline__ uint32_t widen_pair(uint32_t codes, float scale) {
+  const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(codes & 0xFFFFu), __NV_E4M3);
+  const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h));
+  const float2 x = __fmul2_rn(f, make_float2(scale, scale));
+  return pack_bf16x2(x.x, x.y);
+}
+
+// One item of the widening warpgroup: a cache block (64 tokens) of K or of V, 16-byte pieces.
+template <int D>
+struct Item {
+  static constexpr int kSegs = D / 16;                 // 16-code pieces per token
+  static constexpr int kPieces = 64 * kSegs / 128;     // per thread
+  uint4 c[kPieces];
+  float scale;
+
+  // Tokens at or behind `end` are not read and become 0.
+  __device__ __forceinline__ void load(const uint8_t* codes, const float* scales, int tok, int end, int thread) {
+    scale = tok < end ? __ldg(scales + tok / PA_CACHE_BLOCK) : 0.0f;
+#pragma unroll
+    for (int n = 0; n < kPieces; ++n) {
+      const int i = n * 128 + thread;
+      const int j = tok + i / kSegs;
+      c[n] = make_uint4(0u, 0u, 0u, 0u);
+      if (j < end) c[n] = __ldg(reinterpret_cast<const uint4*>(codes + static_cast<size_t>(j) * D + (i % kSegs) * 16));
+    }
+  }
+
+  // Into rows `row0` .. of a swizzled tile: 16-byte chunk c of row r lies at chunk c ^ (r & 7).
+  __device__ __forceinline__ void store(uint8_t* tile, int row0, int thread) const {
+#pragma unroll
+    for (int n = 0; n < kPieces; ++n) {
+      const int i = n * 128 + thread;
+      const int r = row0 + i / kSegs, seg = i % kSegs;
+      const uint32_t w[4] = {c[n].x, c[n].y, c[n].z, c[n].w};
+      uint32_t x[8];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        x[2 * k] = widen_pair(w[k], scale);
+        x[2 * k + 1] = widen_pair(w[k] >> 16, scale);
+      }
+      uint8_t* row = tile + (seg >> 2) * kAtomBytes + r * 128;
+      const int ch = (seg & 3) * 2;
+      // the two atoms share banks: the second one's lanes store their chunks in the other order
+      const int sw = seg >> 2;
+      const uint4 a = make_uint4(x[0], x[1], x[2], x[3]), b = make_uint4(x[4], x[5], x[6], x[7]);
+      *reinterpret_cast<uint4*>(row + (((ch + sw) ^ (r & 7)) << 4)) = sw ? b : a;
+      *reinterpret_cast<uint4*>(row + (((ch + 1 - sw) ^ (r & 7)) << 4)) = sw ? a : b;
+    }
+  }
+};
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1) cache_attn_tc_kernel(const __grid_constant__ CacheAttnTcParams p) {
+  using L = Layout<D>;
+  const CacheAttnParams& prm = p.c;
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t raw = smem_u32(smem_raw);
+  const uint32_t base = (raw + 1023u) & ~1023u;
+  uint8_t* gbase = smem_raw + (base - raw);
+  auto bar = [&](int i) { return base + L::kBar + 8u * i; };
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(gbase + L::kAbort);
+  int* status = prm.status;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+  // Unit: (KV head, 256-row block, split).
+  const int split = blockIdx.x % prm.splits;
+  const int unit = blockIdx.x / prm.splits;
+  const int bh = unit / p.row_blocks;
+  const int row0 = (unit - bh * p.row_blocks) * (2 * kBM);
+  const int nx = prm.R - row0 > kBM ? 2 : 1;
+  const int len = cache_len(prm, bh / prm.Hk);
+  const int chunk = split_chunk(len, prm.splits);
+  const int begin = min(split * chunk, len), end = min(begin + chunk, len);
+  const int T = (end - begin + kBN - 1) / kBN;
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < L::NBAR; ++i) {
+      const bool threads = (i >= L::K_FULL && i < L::K_EMPTY) || (i >= L::P_LO && i < L::O_FINAL) || i >= L::ML_FULL;
+      mbar_init(bar(i), threads ? 128u : 1u);
+    }
+    *abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (warp == 1) {
+    tmem_alloc(base + L::kSlot, 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(gbase + L::kSlot);
+  auto sK = [&](int s) { return base + L::kK + s * L::kTile; };
+  auto sV = [&](int s) { return base + L::kV + s * L::kTile; };
+
+  if (warp < 4) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsLow));
+    if (warp == 0) {
+      if (lane == 0 && T > 0) {
+        mbar_expect_tx(bar(L::Q_FULL), nx * L::kTile);
+        for (int x = 0; x < nx; ++x)
+          tiles::load_tile<D>(base + L::kQ + x * L::kTile, &p.tm_q, row0 + x * kBM, bh, bar(L::Q_FULL));
+        mbar_drain(bar(L::Q_FULL), 0);
+      }
+    } else if (warp == 1 && T > 0) {
+      // ---------------------------------------------------------------- MMA issuer
+      // Per tile j: PV_a(j), S_a(j+1), PV_b(j), S_b(j+1); S_x(j+1) overwrites the P_x(j) that the
+      // product issued before it reads.
+      auto wait = [&](int b, uint32_t parity) { return mbar_wait_warp(bar(b), parity, abort_flag, status); };
+      auto commit = [&](int b) {
+        if (elect_one()) mma_commit(bar(b));
+        __syncwarp();
+      };
+      const uint64_t dq[2] = {tiles::kmajor(base + L::kQ), tiles::kmajor(base + L::kQ + L::kTile)};
+      bool ok = wait(L::Q_FULL, 0) && wait(L::K_FULL, 0) && wait(L::V_FULL, 0);
+      if (ok) {
+        tc_fence_after();
+        for (int x = 0; x < nx; ++x) {
+          tiles::product_nt<D>(tmem + x * 128, dq[x], tiles::kmajor(sK(0)));
+          commit(L::S_FULL + x);
+        }
+        commit(L::K_EMPTY);
+      }
+      int done = 0;
+      for (int j = 0; ok && j < T; ++j) {
+        const int s = j % kStages, s1 = (j + 1) % kStages;
+        const uint32_t ph1 = ((j + 1) / kStages) & 1;
+        const bool more = j + 1 < T;
+        const uint64_t dv = tiles::mnmajor(sV(s)), dk = tiles::kmajor(sK(s1));
+        for (int x = 0; ok && x < nx; ++x) {
+          const uint32_t tP = tmem + x * 128, tO = tmem + 256 + x * 128;
+          if (!(ok = wait(L::P_LO + x, j & 1))) break;
+          tc_fence_after();
+          product_pv<D, 0>(tO, tP, dv, j == 0);
+          // the next operands are checked while P's second half is still being produced
+          if (more && !(ok = x == 0 ? wait(L::K_FULL + s1, ph1) : true)) break;
+          if (more && x == nx - 1 && !(ok = wait(L::V_FULL + s1, ph1))) break;
+          if (!(ok = wait(L::P_HI + x, j & 1))) break;
+          tc_fence_after();
+          product_pv<D, 1>(tO, tP, dv, j == 0);
+          if (!more) commit(L::O_FINAL + x);
+          if (x == nx - 1) commit(L::V_EMPTY + s);
+          if (more) {
+            tiles::product_nt<D>(tP, dq[x], dk);
+            commit(L::S_FULL + x);
+            if (x == nx - 1) commit(L::K_EMPTY + s1);
+          }
+        }
+        if (ok) ++done;
+      }
+      if (lane == 0)                     // the last commits arrive before the CTA exits
+        for (int i = max(0, done - kStages); i < done; ++i) {
+          mbar_drain(bar(L::K_EMPTY + i % kStages), (i / kStages) & 1);
+          mbar_drain(bar(L::V_EMPTY + i % kStages), (i / kStages) & 1);
+        }
+    }
+  } else if (warp < 12) {
+    // ---------------------------------------------------------------- softmax
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsHigh));
+    const int x = (warp - 4) >> 2;
+    const int row = (warp & 3) * 32 + lane;
+    const uint32_t lane_off = static_cast<uint32_t>((warp & 3) * 32) << 16;
+    const uint32_t tS = tmem + lane_off + x * 128, tO = tS + 256;
+    float m = -INFINITY, l = 0.0f;       // running max (log2 units, scaled) and sum
+    const float sl2 = p.scale_log2;
+    for (int j = 0; x < nx && j < T; ++j) {
+      if (!mbar_wait(bar(L::S_FULL + x), j & 1, abort_flag, status)) break;
+      tc_fence_after();
+      float s[kBN];
+      {
+        uint32_t r[2][64];
+        tmem_ld64(tS, r[0]);
+        tmem_ld64(tS + 64, r[1]);
+        tmem_wait_ld();
+#pragma unroll
+        for (int i = 0; i < kBN; ++i) s[i] = __uint_as_float(r[i >> 6][i & 63]);
+      }
+      const int nvalid = end - begin - j * kBN;
+      if (nvalid < kBN) {
+#pragma unroll
+        for (int c = 0; c < kBN; ++c) s[c] = c < nvalid ? s[c] : -INFINITY;
+      }
+      const float mt = row_max(s) * sl2;
+      if (j == 0) {
+        m = mt;
+      } else if (__any_sync(0xffffffffu, mt - m > kRescaleLog2)) {
+        // only rows whose own max grew move it: a row never depends on its neighbours
+        const float m_new = mt - m > kRescaleLog2 ? mt : m;
+        const float alpha = fast_exp2(m - m_new);
+#pragma unroll 1
+        for (int c = 0; c < D / 16; ++c) {
+          uint32_t v[16];
+          tmem_ld16(tO + c * 16, v);
+          tmem_wait_ld();
+#pragma unroll
+          for (int i = 0; i < 16; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) * alpha);
+          tmem_st16(tO + c * 16, v);
+        }
+        l *= alpha;
+        m = m_new;
+      }
+      float2 acc[4] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+      {
+        uint32_t w[32];
+        weights_half<0>(s, m, sl2, acc, w);
+        tmem_st32(tS, w);
+        tmem_wait_st();
+        tc_fence_before();
+        mbar_arrive(bar(L::P_LO + x));
+      }
+      {
+        uint32_t w[32];
+        weights_half<1>(s, m, sl2, acc, w);
+        tmem_st32(tS + 32, w);
+        tmem_wait_st();
+        tc_fence_before();
+        mbar_arrive(bar(L::P_HI + x));
+      }
+      const float2 a = __fadd2_rn(__fadd2_rn(acc[0], acc[1]), __fadd2_rn(acc[2], acc[3]));
+      l += a.x + a.y;
+      if (j == T - 1) {
+        reinterpret_cast<float2*>(gbase + L::kML)[x * kBM + row] = make_float2(m, l);
+        mbar_arrive(bar(L::ML_FULL + x));
+      }
+    }
+  } else {
+    // ---------------------------------------------------------------- widening, then the stores
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsWiden));
+    const int thread = threadIdx.x - 384;
+    const size_t head = static_cast<size_t>(bh) * prm.M * D;
+    const uint8_t* codes[2] = {prm.k_codes + head, prm.v_codes + head};
+    const float* scales[2] = {prm.k_scale + static_cast<size_t>(bh) * prm.blocks,
+                              prm.v_scale + static_cast<size_t>(bh) * prm.blocks};
+    bool ok = true;
+    Item<D> cur;
+    if (T > 0) cur.load(codes[0], scales[0], begin, end, thread);
+    for (int j = 0; ok && j < T; ++j) {
+      const int s = j % kStages;
+      const int tok = begin + j * kBN;
+#pragma unroll
+      for (int kv = 0; kv < 2; ++kv) {
+        if (j >= kStages &&
+            !mbar_wait(bar((kv ? L::V_EMPTY : L::K_EMPTY) + s), (j / kStages - 1) & 1, abort_flag, status)) {
+          ok = false;
+          break;
+        }
+        uint8_t* tile = gbase + (kv ? L::kV : L::kK) + s * L::kTile;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          Item<D> nxt;
+          if (h == 0)
+            nxt.load(codes[kv], scales[kv], tok + 64, end, thread);
+          else if (kv == 0)
+            nxt.load(codes[1], scales[1], tok, end, thread);
+          else
+            nxt.load(codes[0], scales[0], tok + kBN, end, thread);
+          cur.store(tile, h * 64, thread);
+          cur = nxt;
+        }
+        fence_async_smem();
+        mbar_arrive(bar((kv ? L::V_FULL : L::K_FULL) + s));
+      }
+    }
+    const int row = (warp & 3) * 32 + lane;
+    const uint32_t lane_off = static_cast<uint32_t>((warp & 3) * 32) << 16;
+    for (int x = 0; ok && x < nx; ++x) {
+      const int r = row0 + x * kBM + row;
+      const bool row_ok = r < prm.R;
+      const size_t at = (prm.splits > 1 ? static_cast<size_t>(split) * prm.rows : 0) + static_cast<size_t>(bh) * prm.R + r;
+      float2 ml = make_float2(-INFINITY, 1.0f);
+      if (T > 0) {
+        if (!mbar_wait(bar(L::O_FINAL + x), 0, abort_flag, status) ||
+            !mbar_wait(bar(L::ML_FULL + x), 0, abort_flag, status))
+          break;
+        tc_fence_after();
+        ml = reinterpret_cast<const float2*>(gbase + L::kML)[x * kBM + row];
+      }
+      const float inv = 1.0f / ml.y;
+#pragma unroll 1
+      for (int c = 0; c < D / 16; ++c) {
+        uint32_t v[16];
+        if (T > 0) {
+          tmem_ld16(tmem + lane_off + 256 + x * 128 + c * 16, v);
+          tmem_wait_ld();
+        } else {
+#pragma unroll
+          for (int i = 0; i < 16; ++i) v[i] = 0u;
+        }
+        if (row_ok) {
+#pragma unroll
+          for (int i = 0; i < 16; i += 4) {
+            const float4 o = make_float4(__uint_as_float(v[i]) * inv, __uint_as_float(v[i + 1]) * inv,
+                                         __uint_as_float(v[i + 2]) * inv, __uint_as_float(v[i + 3]) * inv);
+            if (prm.splits > 1)
+              store4(prm.ws_o + at * D + c * 16 + i, o);
+            else
+              store4(static_cast<__nv_bfloat16*>(prm.o) + at * D + c * 16 + i, o);
+          }
+        }
+      }
+      if (row_ok) (prm.splits > 1 ? prm.ws_lse : prm.lse)[at] = T > 0 ? (ml.x + fast_log2(ml.y)) * kLn2 : -INFINITY;
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+template <int D>
+int tc_impl(const CacheAttnTcParams& p, unsigned units, cudaStream_t st) {
+  cudaError_t e = cudaFuncSetAttribute(cache_attn_tc_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, Layout<D>::kBytes);
+  if (e != cudaSuccess) return static_cast<int>(e);
+  cache_attn_tc_kernel<D><<<units, kThreads, Layout<D>::kBytes, st>>>(p);
+  return static_cast<int>(cudaGetLastError());
+}
+
+}  // namespace
+
+int cache_attn_tc_block_rows() { return 2 * kBM; }
+
+int launch_cache_attn_tc(const CacheAttnTcParams& p, unsigned units, cudaStream_t st) {
+  return p.c.D == 64 ? tc_impl<64>(p, units, st) : tc_impl<128>(p, units, st);
+}
+
+}  // namespace pa

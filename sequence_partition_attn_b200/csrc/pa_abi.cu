@@ -808,6 +808,9 @@ static int pa_cache_store_impl(pa_ctx* ctx, const pa_cache_store_desc* d, void* 
   return e ? cuda_fail(ctx, e, "cache store launch") : PA_OK;
 }
 
+// bf16 queries take the tcgen05 kernel when a KV head has more than this many query rows.
+static bool cache_attn_many_rows(pa_dtype dtype, long long rows) { return dtype == PA_BF16 && rows > 64; }
+
 // Sizes and the split of the token axis of pa_cache_attn: a rule on sizes alone, so that the
 // scratch can be sized beforehand and a captured call replays with other lengths.
 static int plan_cache_attn(pa_ctx* ctx, pa_dtype dtype, int B, int H, int Hk, int Nq, int M, int D,
@@ -829,11 +832,14 @@ static int plan_cache_attn(pa_ctx* ctx, pa_dtype dtype, int B, int H, int Hk, in
   prm.D = D;
   prm.blocks = (M - 1) / PA_CACHE_BLOCK + 1;
   prm.rows = R * BHk;
-  const int tile_rows = dtype == PA_BF16 ? pa::cache_attn_rows_tile_rows() : pa::cache_attn_f32_tile_rows();
+  const bool many = cache_attn_many_rows(dtype, R);
+  const int tile_rows = many ? pa::cache_attn_tc_block_rows()
+                        : dtype == PA_BF16 ? pa::cache_attn_rows_tile_rows() : pa::cache_attn_f32_tile_rows();
   const long long tiles = BHk * ((R + tile_rows - 1) / tile_rows);
-  // enough blocks to fill the GPU, each with at least four cache blocks of tokens
-  const long long splits = tiles > 0 ? (3LL * ctx->sm_count + tiles - 1) / tiles : 1;
-  prm.splits = static_cast<int>(std::max(1LL, std::min(splits, static_cast<long long>(prm.blocks) / 4)));
+  // enough blocks to fill the GPU (one per SM, or three), each with a few cache blocks of tokens
+  const long long want = many ? ctx->sm_count / std::max(tiles, 1LL)
+                              : (3LL * ctx->sm_count + tiles - 1) / std::max(tiles, 1LL);
+  prm.splits = static_cast<int>(std::max(1LL, std::min(want, static_cast<long long>(prm.blocks) / 4)));
   if (prm.rows > 0x7fffffffLL) return fail(ctx, PA_EINVAL, "too many query rows");
   *ws_bytes = prm.splits > 1 ? static_cast<size_t>(prm.splits) * prm.rows * (D + 1) * sizeof(float) : 0;
   return PA_OK;
@@ -873,7 +879,20 @@ static int pa_cache_attn_impl(pa_ctx* ctx, const pa_cache_attn_desc* d, void* st
     prm.ws_lse = prm.ws_o + static_cast<size_t>(prm.splits) * prm.rows * d->D;
   }
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  int e = d->dtype == PA_BF16 ? pa::launch_cache_attn_rows(prm, st) : pa::launch_cache_attn_f32(prm, st);
+  int e = 0;
+  if (cache_attn_many_rows(d->dtype, prm.R)) {
+    pa::CacheAttnTcParams tc;
+    memset(&tc, 0, sizeof tc);
+    tc.c = prm;
+    tc.row_blocks = (prm.R - 1) / pa::cache_attn_tc_block_rows() + 1;
+    tc.scale_log2 = d->scale * 1.4426950408889634f;
+    if ((rc = encode_qkv_map(ctx, &tc.tm_q, d->q, d->B * d->Hk, prm.R, d->D))) return rc;
+    const long long units = static_cast<long long>(d->B) * d->Hk * tc.row_blocks * prm.splits;
+    if (units > 0x7fffffffLL) return fail(ctx, PA_EINVAL, "too many work units");
+    e = pa::launch_cache_attn_tc(tc, static_cast<unsigned>(units), st);
+  } else {
+    e = d->dtype == PA_BF16 ? pa::launch_cache_attn_rows(prm, st) : pa::launch_cache_attn_f32(prm, st);
+  }
   if (e) return cuda_fail(ctx, e, "cache attention launch");
   if (prm.splits > 1) e = pa::launch_cache_join(prm, d->dtype, st);
   return e ? cuda_fail(ctx, e, "cache join launch") : PA_OK;

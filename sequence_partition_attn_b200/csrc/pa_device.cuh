@@ -425,6 +425,13 @@ struct CacheAttnParams {
   float scale;
 };
 
+struct CacheAttnTcParams {
+  CUtensorMap tm_q;               // {D, R, B * Hk}
+  CacheAttnParams c;
+  int row_blocks;                 // 256-row blocks per KV head
+  float scale_log2;
+};
+
 // The maximal run of selected partitions at or after `from` that holds tokens, as the token
 // range [s0, s1) (neighbouring partitions join); returns where to go on.  s0 == s1 at the end.
 __device__ __forceinline__ int next_range(const AttnTables& t, int g, int from, int& s0, int& s1) {

@@ -49,6 +49,8 @@ int cache_attn_f32_tile_rows();
 int launch_cache_attn_f32(const CacheAttnParams& prm, cudaStream_t st);
 int cache_attn_rows_tile_rows();
 int launch_cache_attn_rows(const CacheAttnParams& prm, cudaStream_t st);
+int cache_attn_tc_block_rows();
+int launch_cache_attn_tc(const CacheAttnTcParams& p, unsigned units, cudaStream_t st);
 int launch_cache_join(const CacheAttnParams& prm, int dtype, cudaStream_t st);
 
 }  // namespace pa
