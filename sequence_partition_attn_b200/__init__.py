@@ -18,6 +18,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 
 import numpy as np
 
@@ -74,32 +75,11 @@ class _MergeDesc(ctypes.Structure):
                 ("w", ctypes.c_void_p), ("cached_per_group", ctypes.c_int)]
 
 
-class _AttnBwdDesc(ctypes.Structure):
-    _fields_ = [("dtype", ctypes.c_int), ("B", ctypes.c_int), ("H", ctypes.c_int),
-                ("N", ctypes.c_int), ("D", ctypes.c_int), ("scale", ctypes.c_float),
-                ("q", ctypes.c_void_p), ("k", ctypes.c_void_p), ("v", ctypes.c_void_p),
-                ("o", ctypes.c_void_p), ("lse", ctypes.c_void_p), ("dout", ctypes.c_void_p),
-                ("dlse", ctypes.c_void_p), ("P", ctypes.c_int), ("part_off", ctypes.c_void_p),
-                ("G", ctypes.c_int), ("fresh", ctypes.c_void_p), ("dq", ctypes.c_void_p),
-                ("dk", ctypes.c_void_p), ("dv", ctypes.c_void_p), ("delta", ctypes.c_void_p)]
-
-
-class _CacheStoreDesc(ctypes.Structure):
-    _fields_ = [("dtype", ctypes.c_int), ("B", ctypes.c_int), ("Hk", ctypes.c_int),
-                ("T", ctypes.c_int), ("M", ctypes.c_int), ("D", ctypes.c_int),
-                ("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("start", ctypes.c_void_p),
-                ("k_codes", ctypes.c_void_p), ("v_codes", ctypes.c_void_p),
-                ("k_scale", ctypes.c_void_p), ("v_scale", ctypes.c_void_p)]
-
-
-class _CacheAttnDesc(ctypes.Structure):
-    _fields_ = [("dtype", ctypes.c_int), ("B", ctypes.c_int), ("H", ctypes.c_int),
-                ("Hk", ctypes.c_int), ("Nq", ctypes.c_int), ("M", ctypes.c_int),
-                ("D", ctypes.c_int), ("scale", ctypes.c_float), ("q", ctypes.c_void_p),
-                ("k_codes", ctypes.c_void_p), ("v_codes", ctypes.c_void_p),
-                ("k_scale", ctypes.c_void_p), ("v_scale", ctypes.c_void_p),
-                ("lens", ctypes.c_void_p), ("o", ctypes.c_void_p), ("lse", ctypes.c_void_p),
-                ("ws", ctypes.c_void_p), ("ws_bytes", ctypes.c_size_t)]
+# The descriptors of the calls below, packed in the C compiler's layout (native alignment) into
+# a bytes object: about a third of a ctypes.Structure's time, which single-token calls notice.
+_ATTN_BWD = struct.Struct("@iiiiif" + "P" * 7 + "iPiP" + "P" * 4)
+_CACHE_STORE = struct.Struct("@iiiiii" + "P" * 7)
+_CACHE_ATTN = struct.Struct("@iiiiiiif" + "P" * 9 + "N")
 
 
 _LIB = None
@@ -132,9 +112,9 @@ def lib():
         L.pa_relayout_seq2head_at.argtypes = [vp, vp, vp, ci, ci, ci, ci, ci, ci, vp]
         L.pa_state_drift.argtypes = [vp, ci, ci, ci, ci, ci, ci, ci, vp, vp, vp, vp, vp, vp, vp]
         L.pa_selftest_wait.argtypes = [vp, ctypes.c_double, vp]
-        L.pa_attn_backward.argtypes = [vp, ctypes.POINTER(_AttnBwdDesc), vp]
-        L.pa_cache_store.argtypes = [vp, ctypes.POINTER(_CacheStoreDesc), vp]
-        L.pa_cache_attn.argtypes = [vp, ctypes.POINTER(_CacheAttnDesc), vp]
+        L.pa_attn_backward.argtypes = [vp, vp, vp]
+        L.pa_cache_store.argtypes = [vp, vp, vp]
+        L.pa_cache_attn.argtypes = [vp, vp, vp]
         L.pa_cache_attn_ws.argtypes = [vp, ci, ci, ci, ci, ci, ci, ci, ctypes.POINTER(ctypes.c_size_t)]
         for f in ("pa_init", "pa_sync_status", "pa_wait_status", "pa_partition_attn", "pa_merge_states", "pa_merge_states_noalloc",
                   "pa_compose_states", "pa_state_drift", "pa_selftest_wait",
@@ -321,15 +301,44 @@ def pa_relayout_seq2head_at(ctx: Context, src, dst, tok0, stream=None):
 
 def _want(ctx, name, t, shape, dtype):
     """Check a tensor argument: the kernels take raw pointers to contiguous device memory."""
-    if tuple(t.shape) != tuple(shape):
+    if t.shape != shape or t.dtype is not dtype or t.get_device() != ctx.device or not t.is_contiguous():
+        _refuse(ctx, name, t, shape, dtype)
+    return t.data_ptr()
+
+
+def _refuse(ctx, name, t, shape, dtype):
+    if t.shape != shape:
         raise PAError(-1, f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
     if t.dtype != dtype:
         raise PAError(-3, f"{name} has dtype {t.dtype}, expected {dtype}")
-    if t.device.type != "cuda" or t.device.index != ctx.device:
+    if t.get_device() != ctx.device:
         raise PAError(-1, f"{name} is on {t.device}, the context on cuda:{ctx.device}")
-    if not t.is_contiguous():
-        raise PAError(-1, f"{name} is not contiguous")
-    return t.data_ptr()
+    raise PAError(-1, f"{name} is not contiguous")
+
+
+def _maybe(ctx, name, t, shape, dtype):
+    return 0 if t is None else _want(ctx, name, t, shape, dtype)
+
+
+def _four(name, t):
+    if t.dim() != 4:
+        raise PAError(-1, f"{name} has shape {tuple(t.shape)}, expected four dimensions")
+    return t.shape
+
+
+def _scale(scale, D):
+    return float(scale) if scale is not None else D ** -0.5
+
+
+def _address(a):
+    return 0 if a is None else a.__array_interface__["data"][0]
+
+
+def _raw_stream(ctx, stream):
+    import torch
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(ctx.device)
+    return stream if isinstance(stream, int) else stream.cuda_stream
 
 
 def pa_attn_backward(ctx: Context, q, k, v, o, lse, do, part_off, G, fresh, dq, dk, dv, delta,
@@ -340,38 +349,36 @@ def pa_attn_backward(ctx: Context, q, k, v, o, lse, do, part_off, G, fresh, dq, 
     receives do.o - dlse and is the call's only scratch.  part_off, G, fresh and scale as in
     the forward call."""
     import torch
-    B, H, N, D = q.shape
+    full = B, H, N, D = _four("q", q)
+    row, dt, f32 = (B, H, N), q.dtype, torch.float32
     code = _dtype_code(q)
-    off, fr = _host_i32(part_off), _host_u8(fresh)
+    off, fr, G = _host_i32(part_off), _host_u8(fresh), int(G)
     _want_mask(off, G, fr)
-    full, row = (B, H, N, D), (B, H, N)
-    ptrs = {n: _want(ctx, n, t, full, q.dtype) for n, t in
-            (("q", q), ("k", k), ("v", v), ("o", o), ("do", do), ("dq", dq), ("dk", dk), ("dv", dv))}
-    rows = {n: None if t is None else _want(ctx, n, t, row, torch.float32) for n, t in
-            (("lse", lse), ("dlse", dlse), ("delta", delta))}
-    d = _AttnBwdDesc(code, B, H, N, D, float(scale if scale is not None else 1.0 / np.sqrt(D)),
-                     ptrs["q"], ptrs["k"], ptrs["v"], ptrs["o"], rows["lse"], ptrs["do"], rows["dlse"],
-                     len(off) - 1, off.ctypes.data, int(G), None if fr is None else fr.ctypes.data,
-                     ptrs["dq"], ptrs["dk"], ptrs["dv"], rows["delta"])
-    _check(ctx.ptr, lib().pa_attn_backward(ctx.ptr, ctypes.byref(d), _stream(stream)))
+    d = _ATTN_BWD.pack(
+        code, B, H, N, D, _scale(scale, D), _want(ctx, "q", q, full, dt), _want(ctx, "k", k, full, dt),
+        _want(ctx, "v", v, full, dt), _want(ctx, "o", o, full, dt), _want(ctx, "lse", lse, row, f32),
+        _want(ctx, "do", do, full, dt), _maybe(ctx, "dlse", dlse, row, f32), off.size - 1, _address(off), G,
+        _address(fr), _want(ctx, "dq", dq, full, dt), _want(ctx, "dk", dk, full, dt),
+        _want(ctx, "dv", dv, full, dt), _want(ctx, "delta", delta, row, f32))
+    _check(ctx.ptr, lib().pa_attn_backward(ctx.ptr, d, _raw_stream(ctx, stream)))
 
 
 def _want_mask(off, G, fr):
     """The C call reads P + 1 offsets and ceil(P / G)^2 mask entries."""
-    P = len(off) - 1
-    if off.ndim != 1 or P < 1 or not 1 <= int(G) <= P:
+    P = off.size - 1
+    if off.ndim != 1 or P < 1 or not 1 <= G <= P:
         raise PAError(-1, f"part_off of {off.size} entries with G={G}")
-    QG = -(-P // int(G))
+    QG = -(-P // G)
     if fr is not None and fr.size != QG * QG:
         raise PAError(-1, f"fresh has {fr.size} entries, expected {QG} x {QG}")
 
 
-def _cache_shapes(ctx, kc, vc, k_scale, v_scale):
+def _cache_args(ctx, kc, vc, k_scale, v_scale):
     import torch
-    B, Hk, M, D = kc.shape
-    code = torch.uint8 if kc.dtype == torch.uint8 else torch.float8_e4m3fn
+    full = B, Hk, M, D = _four("kc", kc)
+    code = torch.uint8 if kc.dtype is torch.uint8 else torch.float8_e4m3fn
     blocks = (B, Hk, -(-M // PA_CACHE_BLOCK))
-    return (B, Hk, M, D, _want(ctx, "kc", kc, (B, Hk, M, D), code), _want(ctx, "vc", vc, (B, Hk, M, D), code),
+    return (B, Hk, M, D, _want(ctx, "kc", kc, full, code), _want(ctx, "vc", vc, full, code),
             _want(ctx, "k_scale", k_scale, blocks, torch.float32),
             _want(ctx, "v_scale", v_scale, blocks, torch.float32))
 
@@ -381,21 +388,20 @@ def pa_cache_store(ctx: Context, k, v, start, kc, vc, k_scale, v_scale, stream=N
     (float8_e4m3fn, or uint8 holding the codes) with scales [B, Hk, ceil(M / 64)] f32, at token
     offsets start (int32 [B] on the device, or None for 0)."""
     import torch
-    B, Hk, M, D, pk, pv, pks, pvs = _cache_shapes(ctx, kc, vc, k_scale, v_scale)
-    T = k.shape[2] if k.dim() == 4 else -1
-    code = _dtype_code(k)
-    d = _CacheStoreDesc(code, B, Hk, T, M, D, _want(ctx, "k", k, (B, Hk, T, D), k.dtype),
-                        _want(ctx, "v", v, (B, Hk, T, D), k.dtype),
-                        None if start is None else _want(ctx, "start", start, (B,), torch.int32),
-                        pk, pv, pks, pvs)
-    _check(ctx.ptr, lib().pa_cache_store(ctx.ptr, ctypes.byref(d), _stream(stream)))
+    B, Hk, M, D, pk, pv, pks, pvs = _cache_args(ctx, kc, vc, k_scale, v_scale)
+    T = _four("k", k)[2]
+    rows = (B, Hk, T, D)
+    d = _CACHE_STORE.pack(_dtype_code(k), B, Hk, T, M, D, _want(ctx, "k", k, rows, k.dtype),
+                          _want(ctx, "v", v, rows, k.dtype), _maybe(ctx, "start", start, (B,), torch.int32),
+                          pk, pv, pks, pvs)
+    _check(ctx.ptr, lib().pa_cache_store(ctx.ptr, d, _raw_stream(ctx, stream)))
 
 
 def cache_attn_workspace(ctx: Context, q, kc):
     """Scratch for pa_cache_attn on tensors of these shapes (uint8, maybe empty).  Calls that
     may overlap on the GPU, and captured graphs that may, need one each."""
     import torch
-    B, H, Nq, D = q.shape
+    B, H, Nq, D = _four("q", q)
     n = ctypes.c_size_t()
     _check(ctx.ptr, lib().pa_cache_attn_ws(ctx.ptr, _dtype_code(q), B, H, kc.shape[1], Nq, kc.shape[2], D,
                                            ctypes.byref(n)))
@@ -409,26 +415,22 @@ def pa_cache_attn(ctx: Context, q, kc, vc, k_scale, v_scale, lens, o, lse, scale
     the cache's Hk.  workspace: from cache_attn_workspace; without one the call takes it from
     torch's allocator."""
     import torch
-    B, Hk, M, D, pk, pv, pks, pvs = _cache_shapes(ctx, kc, vc, k_scale, v_scale)
-    if q.dim() != 4:
-        raise PAError(-1, f"q has shape {tuple(q.shape)}, expected [B, H, Nq, D]")
-    H, Nq = q.shape[1], q.shape[2]
-    code = _dtype_code(q)
-    pq = _want(ctx, "q", q, (B, H, Nq, D), q.dtype)
-    s = _stream(stream)
+    B, Hk, M, D, pk, pv, pks, pvs = _cache_args(ctx, kc, vc, k_scale, v_scale)
+    _, H, Nq, _ = _four("q", q)
+    rows, dt = (B, H, Nq, D), q.dtype
+    pq = _want(ctx, "q", q, rows, dt)
+    s = _raw_stream(ctx, stream)
     if workspace is None:
         workspace = cache_attn_workspace(ctx, q, kc)
         if workspace.numel():
             # allocated for the current stream: not handed out again before `s` is done with it
             workspace.record_stream(torch.cuda.ExternalStream(s, device=workspace.device))
-    else:
-        _want(ctx, "workspace", workspace, (workspace.numel(),), torch.uint8)
-    d = _CacheAttnDesc(code, B, H, Hk, Nq, M, D, float(scale if scale is not None else 1.0 / np.sqrt(D)),
-                       pq, pk, pv, pks, pvs,
-                       None if lens is None else _want(ctx, "lens", lens, (B,), torch.int32),
-                       _want(ctx, "o", o, (B, H, Nq, D), q.dtype), _want(ctx, "lse", lse, (B, H, Nq), torch.float32),
-                       workspace.data_ptr() if workspace.numel() else None, workspace.numel())
-    _check(ctx.ptr, lib().pa_cache_attn(ctx.ptr, ctypes.byref(d), s))
+    size = workspace.numel()
+    d = _CACHE_ATTN.pack(_dtype_code(q), B, H, Hk, Nq, M, D, _scale(scale, D), pq, pk, pv, pks, pvs,
+                         _maybe(ctx, "lens", lens, (B,), torch.int32), _want(ctx, "o", o, rows, dt),
+                         _want(ctx, "lse", lse, (B, H, Nq), torch.float32),
+                         _want(ctx, "workspace", workspace, (size,), torch.uint8) if size else 0, size)
+    _check(ctx.ptr, lib().pa_cache_attn(ctx.ptr, d, s))
 
 
 def select_fresh(w_stored, G: int, threshold: float) -> np.ndarray:
