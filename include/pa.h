@@ -346,7 +346,7 @@ typedef struct {
 /* Attention state of each query row against the first lens[b] tokens of its request's cache:
  *   lse_i = ln sum_j exp(scale q_i . k_j),  o_i = sum_j exp(scale q_i . k_j - lse_i) v_j.
  * Query head h reads KV head h / (H / Hk).  Tokens at or behind lens[b] and the scales of blocks
- * behind it are not read; without any token o = 0, lse = -inf.  With P = 1 the result has the
+ * behind it have no influence, whatever they hold; without any token o = 0, lse = -inf.  With P = 1 the result has the
  * layout of pa_partition_attn's states, so pa_merge_states joins it with others.  The scratch
  * belongs to the caller: calls that may overlap need one each.  A length outside [0, M] is
  * clamped and records PA_EINVAL in the context's status word.  Results do not depend on the

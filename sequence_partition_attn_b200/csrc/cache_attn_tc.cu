@@ -16,7 +16,7 @@
 //   warps 4..7  softmax of query tile a; warps 8..11 of tile b (one row per thread).
 //   warps 12..15 widen K and V; after the last tile they store O and LSE.
 // Rows are the (H / Hk) * Nq queries of one KV head.  A block of at most 128 rows runs tile a only.
-#include <cuda_fp8.h>
+#include <cuda_fp16.h>
 
 #include "mma_tiles.cuh"
 #include "pa_launch.h"
@@ -98,12 +98,14 @@ __device__ __forceinline__ void product_pv(uint32_t o_tmem, uint32_t p_tmem, uin
   }
 }
 
-// Two codes (the low bytes) times a power of two, as a bf16 pair.
-__device__ __forceinline__ uint32_t widen_pair(uint32_t codes, float scale) {
-  const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(codes & 0xFFFFu), __NV_E4M3);
-  const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h));
-  const float2 x = __fmul2_rn(f, make_float2(scale, scale));
-  return pack_bf16x2(x.x, x.y);
+// Four codes times a power of two, as bf16 pairs.
+__device__ __forceinline__ void widen(uint32_t codes, float2 scale, uint32_t& lo, uint32_t& hi) {
+  uint32_t h[2];
+  e4m3_to_f16(codes, h[0], h[1]);
+  const float2 x = __fmul2_rn(__half22float2(*reinterpret_cast<const __half2*>(&h[0])), scale);
+  const float2 y = __fmul2_rn(__half22float2(*reinterpret_cast<const __half2*>(&h[1])), scale);
+  lo = pack_bf16x2(x.x, x.y);
+  hi = pack_bf16x2(y.x, y.y);
 }
 
 // One item of the widening warpgroup: a cache block (64 tokens) of K or of V, 16-byte pieces.
@@ -135,10 +137,7 @@ struct Item {
       const uint32_t w[4] = {c[n].x, c[n].y, c[n].z, c[n].w};
       uint32_t x[8];
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        x[2 * k] = widen_pair(w[k], scale);
-        x[2 * k + 1] = widen_pair(w[k] >> 16, scale);
-      }
+      for (int k = 0; k < 4; ++k) widen(w[k], make_float2(scale, scale), x[2 * k], x[2 * k + 1]);
       uint8_t* row = tile + (seg >> 2) * kAtomBytes + r * 128;
       const int ch = (seg & 3) * 2;
       // the two atoms share banks: the second one's lanes store their chunks in the other order

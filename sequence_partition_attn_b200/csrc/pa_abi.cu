@@ -211,6 +211,21 @@ int encode_qkv_map(pa_ctx* ctx, CUtensorMap* m, const void* ptr, int BH, int N, 
   return PA_OK;
 }
 
+// Codes of the 8-bit cache, `box` tokens at a time, 16-byte chunks swizzled over a row of D bytes.
+int encode_codes_map(pa_ctx* ctx, CUtensorMap* m, const void* ptr, int BHk, int M, int D, int box) {
+  EncodeTiledFn enc = encode_fn();
+  if (!enc) return fail(ctx, PA_ECUDA, "cuTensorMapEncodeTiled unavailable");
+  const cuuint64_t dims[3] = {static_cast<cuuint64_t>(D), static_cast<cuuint64_t>(M), static_cast<cuuint64_t>(BHk)};
+  const cuuint64_t strides[2] = {static_cast<cuuint64_t>(D), static_cast<cuuint64_t>(M) * D};
+  const cuuint32_t boxes[3] = {static_cast<cuuint32_t>(D), static_cast<cuuint32_t>(box), 1};
+  const cuuint32_t estr[3] = {1, 1, 1};
+  CUresult r = enc(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void*>(ptr), dims, strides, boxes, estr,
+                   CU_TENSOR_MAP_INTERLEAVE_NONE, D == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+                   CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS) return fail(ctx, PA_ECUDA, "cuTensorMapEncodeTiled failed (%d)", static_cast<int>(r));
+  return PA_OK;
+}
+
 // Row blocks of the merge / importance kernels per (b, h) and their prefix per query group.
 int fill_blk_start(const pa::AttnTables& t, int* blk_start) {
   const int rpb = pa::merge_rows_per_block();
@@ -832,16 +847,24 @@ static int plan_cache_attn(pa_ctx* ctx, pa_dtype dtype, int B, int H, int Hk, in
   prm.D = D;
   prm.blocks = (M - 1) / PA_CACHE_BLOCK + 1;
   prm.rows = R * BHk;
-  const bool many = cache_attn_many_rows(dtype, R);
-  const int tile_rows = many ? pa::cache_attn_tc_block_rows()
-                        : dtype == PA_BF16 ? pa::cache_attn_rows_tile_rows() : pa::cache_attn_f32_tile_rows();
-  const long long tiles = BHk * ((R + tile_rows - 1) / tile_rows);
-  // enough blocks to fill the GPU (one per SM, or three), each with a few cache blocks of tokens
-  const long long want = many ? ctx->sm_count / std::max(tiles, 1LL)
-                              : (3LL * ctx->sm_count + tiles - 1) / std::max(tiles, 1LL);
-  prm.splits = static_cast<int>(std::max(1LL, std::min(want, static_cast<long long>(prm.blocks) / 4)));
   if (prm.rows > 0x7fffffffLL) return fail(ctx, PA_EINVAL, "too many query rows");
-  *ws_bytes = prm.splits > 1 ? static_cast<size_t>(prm.splits) * prm.rows * (D + 1) * sizeof(float) : 0;
+  *ws_bytes = 0;
+  if (R == 0) return PA_OK;
+  prm.splits = 1;
+  if (dtype == PA_BF16 && !cache_attn_many_rows(dtype, R)) {
+    const int tile = pa::cache_attn_rows_tile_rows(prm.R);
+    prm.row_tiles = (prm.R - 1) / tile + 1;
+    prm.slot_rows = std::min(prm.R, tile);
+    prm.shares = ctx->sm_count * pa::cache_attn_rows_resident(prm.R);
+    *ws_bytes = static_cast<size_t>(prm.shares + BHk * prm.row_tiles) * prm.slot_rows * (D + 1) * sizeof(float);
+    return PA_OK;
+  }
+  const int tile_rows = dtype == PA_BF16 ? pa::cache_attn_tc_block_rows() : pa::cache_attn_f32_tile_rows();
+  const long long tiles = BHk * ((R - 1) / tile_rows + 1);
+  // enough blocks to fill the GPU, each with a few cache blocks of tokens
+  const long long want = (dtype == PA_BF16 ? 1 : 4) * ctx->sm_count / tiles;
+  prm.splits = static_cast<int>(std::max(1LL, std::min(want, static_cast<long long>(prm.blocks) / 4)));
+  if (prm.splits > 1) *ws_bytes = static_cast<size_t>(prm.splits) * prm.rows * (D + 1) * sizeof(float);
   return PA_OK;
 }
 
@@ -876,7 +899,7 @@ static int pa_cache_attn_impl(pa_ctx* ctx, const pa_cache_attn_desc* d, void* st
   prm.scale = d->scale;
   if (need > 0) {
     prm.ws_o = static_cast<float*>(d->ws);
-    prm.ws_lse = prm.ws_o + static_cast<size_t>(prm.splits) * prm.rows * d->D;
+    prm.ws_lse = prm.ws_o + (need / sizeof(float)) / (d->D + 1) * d->D;
   }
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   int e = 0;
@@ -890,8 +913,15 @@ static int pa_cache_attn_impl(pa_ctx* ctx, const pa_cache_attn_desc* d, void* st
     const long long units = static_cast<long long>(d->B) * d->Hk * tc.row_blocks * prm.splits;
     if (units > 0x7fffffffLL) return fail(ctx, PA_EINVAL, "too many work units");
     e = pa::launch_cache_attn_tc(tc, static_cast<unsigned>(units), st);
+  } else if (d->dtype == PA_BF16) {
+    pa::CacheAttnRowsParams rows;
+    memset(&rows, 0, sizeof rows);
+    rows.c = prm;
+    if ((rc = encode_codes_map(ctx, &rows.tm_k, d->k_codes, d->B * d->Hk, d->M, d->D, pa::kCacheRowsBox))) return rc;
+    if ((rc = encode_codes_map(ctx, &rows.tm_v, d->v_codes, d->B * d->Hk, d->M, d->D, pa::kCacheRowsBox))) return rc;
+    e = pa::launch_cache_attn_rows(rows, st);
   } else {
-    e = d->dtype == PA_BF16 ? pa::launch_cache_attn_rows(prm, st) : pa::launch_cache_attn_f32(prm, st);
+    e = pa::launch_cache_attn_f32(prm, st);
   }
   if (e) return cuda_fail(ctx, e, "cache attention launch");
   if (prm.splits > 1) e = pa::launch_cache_join(prm, d->dtype, st);

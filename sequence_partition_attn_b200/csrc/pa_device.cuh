@@ -416,13 +416,20 @@ struct CacheAttnParams {
   const int32_t* lens;            // [B] or null (M)
   void* o;
   float* lse;
-  float* ws_o;                    // [splits][B * Hk * R][D] when splits > 1
-  float* ws_lse;                  // [splits][B * Hk * R]
+  float* ws_o;                    // [splits][B * Hk * R][D] when splits > 1 | [slots][slot_rows][D]
+  float* ws_lse;                  // [splits][B * Hk * R]                    | [slots][slot_rows]
   int* status;
   long long rows;                 // B * Hk * R
   int B, Hk, R, M, D, blocks;
   int splits;                     // of the token axis
+  int row_tiles, shares;          // few rows: 16-row tiles per KV head, equal shares of the work,
+  int slot_rows;                  // rows of a scratch slot (one slot per piece, shares + units at most)
   float scale;
+};
+
+struct CacheAttnRowsParams {
+  CUtensorMap tm_k, tm_v;         // {D, M, B * Hk} codes, boxes of 16 tokens, swizzled over a row
+  CacheAttnParams c;
 };
 
 struct CacheAttnTcParams {
@@ -431,6 +438,16 @@ struct CacheAttnTcParams {
   int row_blocks;                 // 256-row blocks per KV head
   float scale_log2;
 };
+
+// Four e4m3 codes as two f16 pairs, lowest byte first.  Exact: f16 holds every e4m3 value.
+__device__ __forceinline__ void e4m3_to_f16(uint32_t codes, uint32_t& lo, uint32_t& hi) {
+  asm("{\n\t.reg .b16 a, b;\n\t"
+      "mov.b32 {a, b}, %2;\n\t"
+      "cvt.rn.f16x2.e4m3x2 %0, a;\n\t"
+      "cvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
+      : "=r"(lo), "=r"(hi)
+      : "r"(codes));
+}
 
 // The maximal run of selected partitions at or after `from` that holds tokens, as the token
 // range [s0, s1) (neighbouring partitions join); returns where to go on.  s0 == s1 at the end.
@@ -456,7 +473,7 @@ __device__ __forceinline__ int cache_len(const CacheAttnParams& prm, int b) {
   if (!prm.lens) return prm.M;
   const int n = prm.lens[b];
   if (n >= 0 && n <= prm.M) return n;
-  if (threadIdx.x == 0) atomicExch(prm.status, PA_EINVAL);
+  atomicExch(prm.status, PA_EINVAL);
   return n < 0 ? 0 : prm.M;
 }
 
