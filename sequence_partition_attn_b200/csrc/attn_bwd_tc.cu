@@ -32,7 +32,6 @@ using namespace tiles;
 constexpr int kThreads = 384;
 constexpr int kRegsLow = 88, kRegsHigh = 208;
 static_assert(kRegsLow + 2 * kRegsHigh == 3 * 168, "register split must equal the launch allocation");
-constexpr int kStages = 2;
 constexpr float kLog2e = 1.4426950408889634f;
 
 // 64 packed weights -> 32 TMEM columns.
@@ -50,37 +49,75 @@ __device__ __forceinline__ void read_scores(uint32_t tmem, float (&s)[64]) {
   for (int i = 0; i < 64; ++i) s[i] = __uint_as_float(r[i]);
 }
 
+// Whole warp: both phases complete.  A check costs the issuer 110-140 cycles even when the phase is
+// long complete, so the waits of a step are made together.
+struct Phase {
+  uint32_t bar, parity;
+};
+__device__ __forceinline__ bool wait_both(Phase a, Phase b, volatile int* abort_flag, int* status) {
+  const bool now_a = mbar_try_wait(a.bar, a.parity), now_b = mbar_try_wait(b.bar, b.parity);
+  if (__all_sync(0xffffffffu, now_a && now_b)) return true;
+  return mbar_wait_warp(a.bar, a.parity, abort_flag, status) && mbar_wait_warp(b.bar, b.parity, abort_flag, status);
+}
+__device__ __forceinline__ bool wait_three(Phase a, Phase b, Phase c, volatile int* abort_flag, int* status) {
+  const bool now_a = mbar_try_wait(a.bar, a.parity), now_b = mbar_try_wait(b.bar, b.parity),
+             now_c = mbar_try_wait(c.bar, c.parity);
+  if (__all_sync(0xffffffffu, now_a && now_b && now_c)) return true;
+  return mbar_wait_warp(a.bar, a.parity, abort_flag, status) && mbar_wait_warp(b.bar, b.parity, abort_flag, status) &&
+         mbar_wait_warp(c.bar, c.parity, abort_flag, status);
+}
+
+__device__ __forceinline__ bool has_short_range(const AttnTables& t, int g) {
+  for (int p = 0; p < t.P;) {
+    int s0, s1;
+    p = next_range(t, g, p, s0, s1);
+    if (s1 > s0 && s1 - s0 < kRows) return true;
+  }
+  return false;
+}
+
 __device__ __forceinline__ int owner_group(const AttnTables& t, int tile) {
   int g = 0;
   while (g + 1 < t.QG && t.tile_start[g + 1] <= tile) ++g;
   return g;
 }
 
+// Dynamic shared memory starts on a 1024-byte boundary, as the swizzled tiles need (there is no
+// room to move the base).  Checked, and recorded if it ever does not.
+__device__ __forceinline__ bool smem_aligned(uint32_t base, int* status) {
+  if ((base & 1023u) == 0) return true;
+  if (threadIdx.x == 0) atomicExch(status, PA_ECUDA);
+  return false;
+}
+
 // ------------------------------------------------------------------ dK, dV
+// Q(j) is held until dK(j), dO(j) only until dV(j).  (With two stages of each the issuer waited
+// 980 of 3190 cycles per tile for Q.)
+constexpr int kQStages = 3, kOStages = 2;
+
 template <int D>
 struct KvLayout {
   static constexpr int kTile = tile_bytes<D>();
   static constexpr int kK = 0, kV = kTile;
   static constexpr int kQ = 2 * kTile;                        // [stage]
-  static constexpr int kO = kQ + kStages * kTile;             // dO [stage]
-  static constexpr int kStat = kO + kStages * kTile;          // [slot]{-LSE log2e [128], -delta [128]}
+  static constexpr int kO = kQ + kQStages * kTile;            // dO [stage]
+  static constexpr int kStat = kO + kOStages * kTile;         // [slot]{-LSE log2e [128], -delta [128]}
   static constexpr int kBar = kStat + 2 * 2 * kRows * 4;
-  enum { KV_FULL = 0, Q_FULL = 1, O_FULL = Q_FULL + kStages, Q_EMPTY = O_FULL + kStages,
-         O_EMPTY = Q_EMPTY + kStages, STAT_FULL = O_EMPTY + kStages, STAT_EMPTY = STAT_FULL + 2,
+  enum { KV_FULL = 0, Q_FULL = 1, O_FULL = Q_FULL + kQStages, Q_EMPTY = O_FULL + kOStages,
+         O_EMPTY = Q_EMPTY + kQStages, STAT_FULL = O_EMPTY + kOStages, STAT_EMPTY = STAT_FULL + 2,
          S_FULL = STAT_EMPTY + 2, DP_FULL, P_FULL, DS_FULL, FINAL, NBAR };
   static constexpr int kSlot = kBar + NBAR * 8;
   static constexpr int kAbort = kSlot + 8;
-  static constexpr int kBytes = kAbort + 8 + 1024;
+  static constexpr int kBytes = kAbort + 8;
   static_assert(kBytes <= 227 * 1024, "shared memory budget");
 };
 
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1) attn_bwd_kv_kernel(const __grid_constant__ BwdTcParams prm) {
   using L = KvLayout<D>;
-  extern __shared__ uint8_t smem_raw[];
-  const uint32_t raw = smem_u32(smem_raw);
-  const uint32_t base = (raw + 1023u) & ~1023u;
-  uint8_t* gbase = smem_raw + (base - raw);
+  extern __shared__ __align__(1024) uint8_t gbase[];
+  const uint32_t base = smem_u32(gbase);
+  if (!smem_aligned(base, prm.status)) return;
   auto bar = [&](int i) { return base + L::kBar + 8u * i; };
   volatile int* abort_flag = reinterpret_cast<volatile int*>(gbase + L::kAbort);
   int* status = prm.status;
@@ -109,10 +146,10 @@ __global__ void __launch_bounds__(kThreads, 1) attn_bwd_kv_kernel(const __grid_c
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(gbase + L::kSlot);
+  constexpr uint32_t tmem = 0;             // an allocation of all 512 columns starts at column 0
   const uint32_t tX = tmem, tY = tmem + 128, tDV = tmem + 256, tDK = tmem + 384;
   auto sQ = [&](int s) { return base + L::kQ + s * L::kTile; };
-  auto sO = [&](int s) { return base + L::kO + s * L::kTile; };
+  auto sO = [&](int u) { return base + L::kO + u * L::kTile; };
   const int n_tiles = count_tiles(t, g);
 
   if (warp < 4) {
@@ -125,21 +162,20 @@ __global__ void __launch_bounds__(kThreads, 1) attn_bwd_kv_kernel(const __grid_c
         load_tile<D>(base + L::kV, &prm.tm_v, own0, bh, bar(L::KV_FULL));
         int j = 0, nq = 0, no = 0;
         for (TileWalk w(t, g); w.valid(); w.next(), ++j) {
-          const int s = j % kStages;
-          const uint32_t ph = (j / kStages - 1) & 1;
-          if (j >= kStages && !mbar_wait(bar(L::Q_EMPTY + s), ph, abort_flag, status)) break;
+          const int s = j % kQStages, u = j % kOStages;
+          if (j >= kQStages && !mbar_wait(bar(L::Q_EMPTY + s), (j / kQStages - 1) & 1, abort_flag, status)) break;
           mbar_expect_tx(bar(L::Q_FULL + s), L::kTile);
           load_tile<D>(sQ(s), &prm.tm_q, w.row(), bh, bar(L::Q_FULL + s));
           ++nq;
-          if (j >= kStages && !mbar_wait(bar(L::O_EMPTY + s), ph, abort_flag, status)) break;
-          mbar_expect_tx(bar(L::O_FULL + s), L::kTile);
-          load_tile<D>(sO(s), &prm.tm_do, w.row(), bh, bar(L::O_FULL + s));
+          if (j >= kOStages && !mbar_wait(bar(L::O_EMPTY + u), (j / kOStages - 1) & 1, abort_flag, status)) break;
+          mbar_expect_tx(bar(L::O_FULL + u), L::kTile);
+          load_tile<D>(sO(u), &prm.tm_do, w.row(), bh, bar(L::O_FULL + u));
           ++no;
         }
         // every load issued lands before the CTA exits
         mbar_drain(bar(L::KV_FULL), 0);
-        for (int i = max(0, nq - kStages); i < nq; ++i) mbar_drain(bar(L::Q_FULL + i % kStages), (i / kStages) & 1);
-        for (int i = max(0, no - kStages); i < no; ++i) mbar_drain(bar(L::O_FULL + i % kStages), (i / kStages) & 1);
+        for (int i = max(0, nq - kQStages); i < nq; ++i) mbar_drain(bar(L::Q_FULL + i % kQStages), (i / kQStages) & 1);
+        for (int i = max(0, no - kOStages); i < no; ++i) mbar_drain(bar(L::O_FULL + i % kOStages), (i / kOStages) & 1);
       }
     } else if (warp == 1) {
       // ---------------------------------------------------------------- MMA issuer
@@ -151,35 +187,43 @@ __global__ void __launch_bounds__(kThreads, 1) attn_bwd_kv_kernel(const __grid_c
           __syncwarp();
         };
         TileWalk w(t, g);
-        // the operands of tile j are in shared memory, and zero behind a short range
-        auto ready = [&](int j) {
-          const int s = j % kStages;
-          const uint32_t ph = (j / kStages) & 1;
-          if (!wait(L::Q_FULL + s, ph) || !wait(L::O_FULL + s, ph)) return false;
+        const bool shorts = has_short_range(t, g);
+        auto phase = [&](int b, uint32_t parity) { return Phase{bar(b), parity & 1}; };
+        // Tile j's operands arrived: zero behind a short range.
+        auto fix = [&](int s, int u) {
           if (w.is_short()) {
             zero_rows<D>(gbase + L::kQ + s * L::kTile, w.last(), lane);
-            zero_rows<D>(gbase + L::kO + s * L::kTile, w.last(), lane);
+            zero_rows<D>(gbase + L::kO + u * L::kTile, w.last(), lane);
           }
           w.next();
-          tc_fence_after();
-          return true;
         };
-        bool ok = wait(L::KV_FULL, 0) && ready(0);
+        bool ok = wait(L::KV_FULL, 0) && wait(L::Q_FULL, 0) && wait(L::O_FULL, 0);
         int done = 0;                    // tiles whose Q_EMPTY, O_EMPTY commits were issued
         if (ok) {
+          if (shorts) fix(0, 0);
+          tc_fence_after();
           product_nt<D>(tX, aK, kmajor(sQ(0)));
           commit(L::S_FULL);
           product_nt<D>(tY, aV, kmajor(sO(0)));
           commit(L::DP_FULL);
         }
+        int s = 0, u = 0;                // stages of Q(j), dO(j)
+        uint32_t phq = 0;                // parity of Q(j + 1)
         for (int j = 0; ok && j < n_tiles; ++j) {
-          const int s = j % kStages, s1 = (j + 1) % kStages;
+          const int s1 = s + 1 == kQStages ? 0 : s + 1, u1 = u ^ 1;
           const bool more = j + 1 < n_tiles;
-          if (more && !(ok = ready(j + 1))) break;
-          if (!(ok = wait(L::P_FULL, j & 1))) break;
+          if (s1 == 0) phq ^= 1;
+          if (more) {
+            ok = wait_three(phase(L::P_FULL, j), phase(L::Q_FULL + s1, phq), phase(L::O_FULL + u1, (j + 1) / kOStages),
+                            abort_flag, status);
+            if (ok && shorts) fix(s1, u1);
+          } else {
+            ok = wait(L::P_FULL, j & 1);
+          }
+          if (!ok) break;
           tc_fence_after();
-          product_w<D>(tDV, tX, mnmajor(sO(s)), j == 0);
-          commit(L::O_EMPTY + s);
+          product_w<D>(tDV, tX, mnmajor(sO(u)), j == 0);
+          commit(L::O_EMPTY + u);
           if (more) {
             product_nt<D>(tX, aK, kmajor(sQ(s1)));
             commit(L::S_FULL);
@@ -190,17 +234,18 @@ __global__ void __launch_bounds__(kThreads, 1) attn_bwd_kv_kernel(const __grid_c
           commit(L::Q_EMPTY + s);
           ++done;
           if (more) {
-            product_nt<D>(tY, aV, kmajor(sO(s1)));
+            product_nt<D>(tY, aV, kmajor(sO(u1)));
             commit(L::DP_FULL);
           } else {
             commit(L::FINAL);
           }
+          s = s1;
+          u = u1;
         }
-        if (lane == 0)                   // the last commits arrive before the CTA exits
-          for (int i = max(0, done - kStages); i < done; ++i) {
-            mbar_drain(bar(L::O_EMPTY + i % kStages), (i / kStages) & 1);
-            mbar_drain(bar(L::Q_EMPTY + i % kStages), (i / kStages) & 1);
-          }
+        if (lane == 0) {                 // the last commits arrive before the CTA exits
+          for (int i = max(0, done - kOStages); i < done; ++i) mbar_drain(bar(L::O_EMPTY + i % kOStages), (i / kOStages) & 1);
+          for (int i = max(0, done - kQStages); i < done; ++i) mbar_drain(bar(L::Q_EMPTY + i % kQStages), (i / kQStages) & 1);
+        }
       }
     } else if (warp == 3) {
       // ---------------------------------------------------------------- LSE and delta
@@ -324,17 +369,16 @@ struct QLayout {
          DP_FULL = S_FULL + 2, S_READ = DP_FULL + 2, DS_FULL = S_READ + 2, FINAL = DS_FULL + 2, NBAR };
   static constexpr int kSlot = kBar + NBAR * 8;
   static constexpr int kAbort = kSlot + 8;
-  static constexpr int kBytes = kAbort + 8 + 1024;
+  static constexpr int kBytes = kAbort + 8;
   static_assert(kBytes <= 227 * 1024, "shared memory budget");
 };
 
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1) attn_bwd_q_kernel(const __grid_constant__ BwdTcParams prm) {
   using L = QLayout<D>;
-  extern __shared__ uint8_t smem_raw[];
-  const uint32_t raw = smem_u32(smem_raw);
-  const uint32_t base = (raw + 1023u) & ~1023u;
-  uint8_t* gbase = smem_raw + (base - raw);
+  extern __shared__ __align__(1024) uint8_t gbase[];
+  const uint32_t base = smem_u32(gbase);
+  if (!smem_aligned(base, prm.status)) return;
   auto bar = [&](int i) { return base + L::kBar + 8u * i; };
   volatile int* abort_flag = reinterpret_cast<volatile int*>(gbase + L::kAbort);
   int* status = prm.status;
@@ -359,7 +403,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_bwd_q_kernel(const __grid_co
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(gbase + L::kSlot);
+  constexpr uint32_t tmem = 0;             // an allocation of all 512 columns starts at column 0
   const uint32_t tDQ = tmem + 384;
   auto region = [&](int i) { return tmem + 128u * (i % 3); };
   auto sK = [&](int j) { return base + L::kK + (j % kKStages) * L::kTile; };
@@ -400,37 +444,67 @@ __global__ void __launch_bounds__(kThreads, 1) attn_bwd_q_kernel(const __grid_co
           __syncwarp();
         };
         TileWalk wk(t, g), wv(t, g);
-        // K(j), V(j) in shared memory, and zero behind a short range
-        auto issue_s = [&](int j) {
-          if (!wait(L::K_FULL + j % kKStages, (j / kKStages) & 1)) return false;
-          if (wk.is_short()) zero_rows<D>(gbase + (sK(j) - base), wk.last(), lane);
-          wk.next();
-          tc_fence_after();
-          product_nt<D>(region(2 * j), aQ, kmajor(sK(j)));
-          commit(L::S_FULL + (j & 1));
-          return true;
+        const bool shorts = has_short_range(t, g);
+        auto phase = [&](int b, uint32_t parity) { return Phase{bar(b), parity & 1}; };
+        // A tile arrived: zero behind a short range.
+        auto fix = [&](TileWalk& w, int at) {
+          if (w.is_short()) zero_rows<D>(gbase + at, w.last(), lane);
+          w.next();
         };
-        auto issue_dp = [&](int j) {
-          if (!wait(L::V_FULL + j % kVStages, (j / kVStages) & 1)) return false;
-          if (wv.is_short()) zero_rows<D>(gbase + (sV(j) - base), wv.last(), lane);
-          wv.next();
-          tc_fence_after();
-          product_nt<D>(region(2 * j + 1), aO, kmajor(sV(j)));
-          commit(L::V_EMPTY + j % kVStages);
-          commit(L::DP_FULL + (j & 1));
-          return true;
-        };
-        bool ok = wait(L::OWN_FULL, 0) && issue_s(0) && issue_dp(0) && (n_tiles < 2 || issue_s(1));
+        bool ok = wait(L::OWN_FULL, 0) && wait(L::K_FULL, 0) && wait(L::V_FULL, 0) && (n_tiles < 2 || wait(L::K_FULL + 1, 0));
         int done = 0;
-        for (int j = 0; ok && j < n_tiles; ++j) {
-          if (j + 1 < n_tiles && !(ok = wait(L::S_READ + (j & 1), (j / 2) & 1) && issue_dp(j + 1))) break;
-          if (!(ok = wait(L::DS_FULL + (j & 1), (j / 2) & 1))) break;
+        if (ok) {
+          if (shorts) {
+            fix(wk, L::kK);
+            fix(wv, L::kV);
+            if (n_tiles > 1) fix(wk, L::kK + L::kTile);
+          }
           tc_fence_after();
-          product_w<D>(tDQ, region(2 * j + 1), mnmajor(sK(j)), j == 0);
-          commit(L::K_EMPTY + j % kKStages);
+          product_nt<D>(region(0), aQ, kmajor(sK(0)));
+          commit(L::S_FULL);
+          product_nt<D>(region(1), aO, kmajor(sV(0)));
+          commit(L::V_EMPTY);
+          commit(L::DP_FULL);
+          if (n_tiles > 1) {
+            product_nt<D>(region(2), aQ, kmajor(sK(1)));
+            commit(L::S_FULL + 1);
+          }
+        }
+        int s = 0, r = 0;                // stage of K(j); region of S(j)
+        uint32_t phk = 0;                // parity of K(j + 2)
+        for (int j = 0; ok && j < n_tiles; ++j) {
+          const int b = j & 1;
+          const uint32_t ph = j / 2;
+          const int s2 = s == 0 ? 2 : s - 1;                  // stage of K(j + 2)
+          if (s2 == 0) phk ^= 1;
+          const uint32_t tS = tmem + 128 * r, tP = tmem + 128 * (r == 2 ? 0 : r + 1);
+          if (j + 1 < n_tiles) {
+            ok = wait_both(phase(L::S_READ + b, ph), phase(L::V_FULL + (b ^ 1), (j + 1) / kVStages), abort_flag, status);
+            if (!ok) break;
+            if (shorts) fix(wv, L::kV + (b ^ 1) * L::kTile);
+            tc_fence_after();
+            product_nt<D>(tS, aO, kmajor(base + L::kV + (b ^ 1) * L::kTile));       // dP(j + 1) over S(j)
+            commit(L::V_EMPTY + (b ^ 1));
+            commit(L::DP_FULL + (b ^ 1));
+          }
+          if (j + 2 < n_tiles) {
+            ok = wait_both(phase(L::DS_FULL + b, ph), phase(L::K_FULL + s2, phk), abort_flag, status);
+            if (ok && shorts) fix(wk, L::kK + s2 * L::kTile);
+          } else {
+            ok = wait(L::DS_FULL + b, ph & 1);
+          }
+          if (!ok) break;
+          tc_fence_after();
+          product_w<D>(tDQ, tP, mnmajor(base + L::kK + s * L::kTile), j == 0);
+          commit(L::K_EMPTY + s);
           ++done;
+          if (j + 2 < n_tiles) {
+            product_nt<D>(tP, aQ, kmajor(base + L::kK + s2 * L::kTile));            // S(j + 2) over dS(j)
+            commit(L::S_FULL + b);
+          }
           if (j + 1 == n_tiles) commit(L::FINAL);
-          if (j + 2 < n_tiles) ok = issue_s(j + 2);
+          s = s == kKStages - 1 ? 0 : s + 1;
+          r = r == 0 ? 2 : r - 1;                             // 2 (j + 1) % 3
         }
         if (lane == 0)
           for (int i = max(0, done - kKStages); i < done; ++i)
