@@ -1,7 +1,7 @@
 // attn_bwd_tc.cu -- bf16 backward pass of attention with reuse on sm_100a tensor cores
 // (tcgen05 + TMEM + TMA).  The mathematics is at the top of attn_bwd.cu.
 //
-// Two kernels, each owning a 128-row tile and streaming 128-row tiles of the other side over the
+// Two kinds of CTA, each owning a 128-row tile and streaming 128-row tiles of the other side over the
 // fresh ranges of its group (neighbouring partitions join: the gradient needs no partition
 // states).  No atomics: a tile's sums belong to one CTA, in a fixed order.
 //
@@ -49,24 +49,6 @@ __device__ __forceinline__ void read_scores(uint32_t tmem, float (&s)[64]) {
   for (int i = 0; i < 64; ++i) s[i] = __uint_as_float(r[i]);
 }
 
-// Whole warp: both phases complete.  A check costs the issuer 110-140 cycles even when the phase is
-// long complete, so the waits of a step are made together.
-struct Phase {
-  uint32_t bar, parity;
-};
-__device__ __forceinline__ bool wait_both(Phase a, Phase b, volatile int* abort_flag, int* status) {
-  const bool now_a = mbar_try_wait(a.bar, a.parity), now_b = mbar_try_wait(b.bar, b.parity);
-  if (__all_sync(0xffffffffu, now_a && now_b)) return true;
-  return mbar_wait_warp(a.bar, a.parity, abort_flag, status) && mbar_wait_warp(b.bar, b.parity, abort_flag, status);
-}
-__device__ __forceinline__ bool wait_three(Phase a, Phase b, Phase c, volatile int* abort_flag, int* status) {
-  const bool now_a = mbar_try_wait(a.bar, a.parity), now_b = mbar_try_wait(b.bar, b.parity),
-             now_c = mbar_try_wait(c.bar, c.parity);
-  if (__all_sync(0xffffffffu, now_a && now_b && now_c)) return true;
-  return mbar_wait_warp(a.bar, a.parity, abort_flag, status) && mbar_wait_warp(b.bar, b.parity, abort_flag, status) &&
-         mbar_wait_warp(c.bar, c.parity, abort_flag, status);
-}
-
 __device__ __forceinline__ bool has_short_range(const AttnTables& t, int g) {
   for (int p = 0; p < t.P;) {
     int s0, s1;
@@ -76,9 +58,16 @@ __device__ __forceinline__ bool has_short_range(const AttnTables& t, int g) {
   return false;
 }
 
-__device__ __forceinline__ int owner_group(const AttnTables& t, int tile) {
-  int g = 0;
-  while (g + 1 < t.QG && t.tile_start[g + 1] <= tile) ++g;
+// The group, head and first row of a unit: groups in launch order, heads and then tiles in each.
+__device__ __forceinline__ int owner_tile(const BwdSide& side, int unit, int& bh, int& own0) {
+  int i = 0;
+  while (side.unit_start[i + 1] <= unit) ++i;
+  const int g = side.order[i];
+  const int rows = side.t.qg_row0[g + 1] - side.t.qg_row0[g];
+  const int tiles = (rows + kRows - 1) / kRows;
+  const int local = unit - side.unit_start[i];
+  bh = local / tiles;
+  own0 = side.t.qg_row0[g] + (local - bh * tiles) * kRows;
   return g;
 }
 
@@ -105,7 +94,7 @@ struct KvLayout {
   static constexpr int kBar = kStat + 2 * 2 * kRows * 4;
   enum { KV_FULL = 0, Q_FULL = 1, O_FULL = Q_FULL + kQStages, Q_EMPTY = O_FULL + kOStages,
          O_EMPTY = Q_EMPTY + kQStages, STAT_FULL = O_EMPTY + kOStages, STAT_EMPTY = STAT_FULL + 2,
-         S_FULL = STAT_EMPTY + 2, DP_FULL, P_FULL, DS_FULL, FINAL, NBAR };
+         S_FULL = STAT_EMPTY + 2, DP_FULL, P_LO, P_HI, DS_FULL, FINAL, NBAR };
   static constexpr int kSlot = kBar + NBAR * 8;
   static constexpr int kAbort = kSlot + 8;
   static constexpr int kBytes = kAbort + 8;
@@ -113,27 +102,22 @@ struct KvLayout {
 };
 
 template <int D>
-__global__ void __launch_bounds__(kThreads, 1) attn_bwd_kv_kernel(const __grid_constant__ BwdTcParams prm) {
+__device__ __forceinline__ void dkdv_unit(const BwdTcParams& prm, int unit, uint8_t* gbase, const uint32_t base) {
   using L = KvLayout<D>;
-  extern __shared__ __align__(1024) uint8_t gbase[];
-  const uint32_t base = smem_u32(gbase);
-  if (!smem_aligned(base, prm.status)) return;
   auto bar = [&](int i) { return base + L::kBar + 8u * i; };
   volatile int* abort_flag = reinterpret_cast<volatile int*>(gbase + L::kAbort);
   int* status = prm.status;
-  const AttnTables& t = prm.t;
+  const AttnTables& t = prm.kv.t;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int bh = blockIdx.x / prm.tiles_total;
-  const int tile = blockIdx.x - bh * prm.tiles_total;
-  const int g = owner_group(t, tile);
-  const int own0 = t.qg_row0[g] + (tile - t.tile_start[g]) * kRows;
+  int bh, own0;
+  const int g = owner_tile(prm.kv, unit, bh, own0);
   const int own1 = t.qg_row0[g + 1];
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < L::NBAR; ++i) {
       uint32_t n = 1;
       if (i == L::STAT_FULL || i == L::STAT_FULL + 1) n = 32;
-      if (i == L::STAT_EMPTY || i == L::STAT_EMPTY + 1 || i == L::P_FULL || i == L::DS_FULL) n = 256;
+      if (i == L::STAT_EMPTY || i == L::STAT_EMPTY + 1 || i == L::P_LO || i == L::P_HI || i == L::DS_FULL) n = 256;
       mbar_init(bar(i), n);
     }
     *abort_flag = 0;
@@ -179,21 +163,17 @@ __global__ void __launch_bounds__(kThreads, 1) attn_bwd_kv_kernel(const __grid_c
       }
     } else if (warp == 1) {
       // ---------------------------------------------------------------- MMA issuer
-      if (n_tiles > 0) {
+      if (n_tiles > 0 && elect_one()) {
         const uint64_t aK = kmajor(base + L::kK), aV = kmajor(base + L::kV);
-        auto wait = [&](int b, uint32_t parity) { return mbar_wait_warp(bar(b), parity, abort_flag, status); };
-        auto commit = [&](int b) {
-          if (elect_one()) mma_commit(bar(b));
-          __syncwarp();
-        };
+        auto wait = [&](int b, uint32_t parity) { return mbar_wait(bar(b), parity & 1, abort_flag, status); };
+        auto commit = [&](int b) { mma_commit(bar(b)); };
         TileWalk w(t, g);
         const bool shorts = has_short_range(t, g);
-        auto phase = [&](int b, uint32_t parity) { return Phase{bar(b), parity & 1}; };
         // Tile j's operands arrived: zero behind a short range.
         auto fix = [&](int s, int u) {
           if (w.is_short()) {
-            zero_rows<D>(gbase + L::kQ + s * L::kTile, w.last(), lane);
-            zero_rows<D>(gbase + L::kO + u * L::kTile, w.last(), lane);
+            zero_rows<D>(gbase + L::kQ + s * L::kTile, w.last());
+            zero_rows<D>(gbase + L::kO + u * L::kTile, w.last());
           }
           w.next();
         };
@@ -214,15 +194,17 @@ __global__ void __launch_bounds__(kThreads, 1) attn_bwd_kv_kernel(const __grid_c
           const bool more = j + 1 < n_tiles;
           if (s1 == 0) phq ^= 1;
           if (more) {
-            ok = wait_three(phase(L::P_FULL, j), phase(L::Q_FULL + s1, phq), phase(L::O_FULL + u1, (j + 1) / kOStages),
-                            abort_flag, status);
+            ok = wait(L::Q_FULL + s1, phq) && wait(L::O_FULL + u1, (j + 1) / kOStages) && wait(L::P_LO, j);
             if (ok && shorts) fix(s1, u1);
           } else {
-            ok = wait(L::P_FULL, j & 1);
+            ok = wait(L::P_LO, j);
           }
           if (!ok) break;
           tc_fence_after();
-          product_w<D>(tDV, tX, mnmajor(sO(u)), j == 0);
+          product_w<D, 64, 0x33>(tDV, tX, mnmajor(sO(u)), j == 0);      // columns 0-31 and 64-95 of P
+          if (!(ok = wait(L::P_HI, j))) break;
+          tc_fence_after();
+          product_w<D, 64, 0xCC>(tDV, tX, mnmajor(sO(u)), false);
           commit(L::O_EMPTY + u);
           if (more) {
             product_nt<D>(tX, aK, kmajor(sQ(s1)));
@@ -230,7 +212,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_bwd_kv_kernel(const __grid_c
           }
           if (!(ok = wait(L::DS_FULL, j & 1))) break;
           tc_fence_after();
-          product_w<D>(tDK, tY, mnmajor(sQ(s)), j == 0);
+          product_w<D, 64>(tDK, tY, mnmajor(sQ(s)), j == 0);
           commit(L::Q_EMPTY + s);
           ++done;
           if (more) {
@@ -242,7 +224,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_bwd_kv_kernel(const __grid_c
           s = s1;
           u = u1;
         }
-        if (lane == 0) {                 // the last commits arrive before the CTA exits
+        {                                // the last commits arrive before the CTA exits
           for (int i = max(0, done - kOStages); i < done; ++i) mbar_drain(bar(L::O_EMPTY + i % kOStages), (i / kOStages) & 1);
           for (int i = max(0, done - kQStages); i < done; ++i) mbar_drain(bar(L::Q_EMPTY + i % kQStages), (i / kQStages) & 1);
         }
@@ -293,19 +275,27 @@ __global__ void __launch_bounds__(kThreads, 1) attn_bwd_kv_kernel(const __grid_c
       read_scores(sX, p);
       uint32_t w[32];
 #pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        const float4 l = nl[i];
-        const float2 a = __ffma2_rn(make_float2(p[4 * i], p[4 * i + 1]), scale2, make_float2(l.x, l.y));
-        const float2 b = __ffma2_rn(make_float2(p[4 * i + 2], p[4 * i + 3]), scale2, make_float2(l.z, l.w));
-        p[4 * i] = fast_exp2(a.x);
-        p[4 * i + 1] = fast_exp2(a.y);
-        p[4 * i + 2] = fast_exp2(b.x);
-        p[4 * i + 3] = fast_exp2(b.y);
-        w[2 * i] = pack_bf16x2(p[4 * i], p[4 * i + 1]);
-        w[2 * i + 1] = pack_bf16x2(p[4 * i + 2], p[4 * i + 3]);
+      for (int h = 0; h < 2; ++h) {          // handed over in halves: dV starts on the first
+#pragma unroll
+        for (int i = 8 * h; i < 8 * h + 8; ++i) {
+          const float4 l = nl[i];
+          const float2 a = __ffma2_rn(make_float2(p[4 * i], p[4 * i + 1]), scale2, make_float2(l.x, l.y));
+          const float2 b = __ffma2_rn(make_float2(p[4 * i + 2], p[4 * i + 3]), scale2, make_float2(l.z, l.w));
+          p[4 * i] = fast_exp2(a.x);
+          p[4 * i + 1] = fast_exp2(a.y);
+          p[4 * i + 2] = fast_exp2(b.x);
+          p[4 * i + 3] = fast_exp2(b.y);
+          w[2 * i] = pack_bf16x2(p[4 * i], p[4 * i + 1]);
+          w[2 * i + 1] = pack_bf16x2(p[4 * i + 2], p[4 * i + 3]);
+        }
+        uint32_t half[16];
+#pragma unroll
+        for (int i = 0; i < 16; ++i) half[i] = w[16 * h + i];
+        tmem_st16(sX + 16 * h, half);
+        tmem_wait_st();
+        tc_fence_before();
+        mbar_arrive(bar(h ? L::P_HI : L::P_LO));
       }
-      store_weights(sX, w);
-      mbar_arrive(bar(L::P_FULL));
       if (!mbar_wait(bar(L::DP_FULL), j & 1, abort_flag, status)) {
         ok = false;
         break;
@@ -328,7 +318,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_bwd_kv_kernel(const __grid_c
       mbar_arrive(bar(L::STAT_EMPTY + slot));
     }
     // warpgroup 0 stores dV, warpgroup 1 dK
-    __nv_bfloat16* out = static_cast<__nv_bfloat16*>(x ? prm.out0 : prm.out1) +
+    __nv_bfloat16* out = static_cast<__nv_bfloat16*>(x ? prm.dk : prm.dv) +
                          (static_cast<size_t>(bh) * prm.N + own0 + row) * D;
     const bool row_ok = own0 + row < own1;
     if (n_tiles == 0) {
@@ -374,20 +364,15 @@ struct QLayout {
 };
 
 template <int D>
-__global__ void __launch_bounds__(kThreads, 1) attn_bwd_q_kernel(const __grid_constant__ BwdTcParams prm) {
+__device__ __forceinline__ void dq_unit(const BwdTcParams& prm, int unit, uint8_t* gbase, const uint32_t base) {
   using L = QLayout<D>;
-  extern __shared__ __align__(1024) uint8_t gbase[];
-  const uint32_t base = smem_u32(gbase);
-  if (!smem_aligned(base, prm.status)) return;
   auto bar = [&](int i) { return base + L::kBar + 8u * i; };
   volatile int* abort_flag = reinterpret_cast<volatile int*>(gbase + L::kAbort);
   int* status = prm.status;
-  const AttnTables& t = prm.t;
+  const AttnTables& t = prm.q.t;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int bh = blockIdx.x / prm.tiles_total;
-  const int tile = blockIdx.x - bh * prm.tiles_total;
-  const int g = owner_group(t, tile);
-  const int own0 = t.qg_row0[g] + (tile - t.tile_start[g]) * kRows;
+  int bh, own0;
+  const int g = owner_tile(prm.q, unit, bh, own0);
   const int own1 = t.qg_row0[g + 1];
 
   if (threadIdx.x == 0) {
@@ -436,19 +421,15 @@ __global__ void __launch_bounds__(kThreads, 1) attn_bwd_q_kernel(const __grid_co
       }
     } else if (warp == 1) {
       // ---------------------------------------------------------------- MMA issuer
-      if (n_tiles > 0) {
+      if (n_tiles > 0 && elect_one()) {
         const uint64_t aQ = kmajor(base + L::kQ), aO = kmajor(base + L::kO);
-        auto wait = [&](int b, uint32_t parity) { return mbar_wait_warp(bar(b), parity, abort_flag, status); };
-        auto commit = [&](int b) {
-          if (elect_one()) mma_commit(bar(b));
-          __syncwarp();
-        };
+        auto wait = [&](int b, uint32_t parity) { return mbar_wait(bar(b), parity & 1, abort_flag, status); };
+        auto commit = [&](int b) { mma_commit(bar(b)); };
         TileWalk wk(t, g), wv(t, g);
         const bool shorts = has_short_range(t, g);
-        auto phase = [&](int b, uint32_t parity) { return Phase{bar(b), parity & 1}; };
         // A tile arrived: zero behind a short range.
         auto fix = [&](TileWalk& w, int at) {
-          if (w.is_short()) zero_rows<D>(gbase + at, w.last(), lane);
+          if (w.is_short()) zero_rows<D>(gbase + at, w.last());
           w.next();
         };
         bool ok = wait(L::OWN_FULL, 0) && wait(L::K_FULL, 0) && wait(L::V_FULL, 0) && (n_tiles < 2 || wait(L::K_FULL + 1, 0));
@@ -479,7 +460,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_bwd_q_kernel(const __grid_co
           if (s2 == 0) phk ^= 1;
           const uint32_t tS = tmem + 128 * r, tP = tmem + 128 * (r == 2 ? 0 : r + 1);
           if (j + 1 < n_tiles) {
-            ok = wait_both(phase(L::S_READ + b, ph), phase(L::V_FULL + (b ^ 1), (j + 1) / kVStages), abort_flag, status);
+            ok = wait(L::V_FULL + (b ^ 1), (j + 1) / kVStages) && wait(L::S_READ + b, ph);
             if (!ok) break;
             if (shorts) fix(wv, L::kV + (b ^ 1) * L::kTile);
             tc_fence_after();
@@ -487,18 +468,16 @@ __global__ void __launch_bounds__(kThreads, 1) attn_bwd_q_kernel(const __grid_co
             commit(L::V_EMPTY + (b ^ 1));
             commit(L::DP_FULL + (b ^ 1));
           }
-          if (j + 2 < n_tiles) {
-            ok = wait_both(phase(L::DS_FULL + b, ph), phase(L::K_FULL + s2, phk), abort_flag, status);
-            if (ok && shorts) fix(wk, L::kK + s2 * L::kTile);
-          } else {
-            ok = wait(L::DS_FULL + b, ph & 1);
-          }
-          if (!ok) break;
+          if (!(ok = wait(L::DS_FULL + b, ph))) break;
           tc_fence_after();
-          product_w<D>(tDQ, tP, mnmajor(base + L::kK + s * L::kTile), j == 0);
+          product_w<D, 64>(tDQ, tP, mnmajor(base + L::kK + s * L::kTile), j == 0);
           commit(L::K_EMPTY + s);
           ++done;
           if (j + 2 < n_tiles) {
+            // K(j + 2) takes the stage of K(j - 1), which dQ(j - 1) has just released: dQ(j) covers the load
+            if (!(ok = wait(L::K_FULL + s2, phk))) break;
+            if (shorts) fix(wk, L::kK + s2 * L::kTile);
+            tc_fence_after();
             product_nt<D>(tP, aQ, kmajor(base + L::kK + s2 * L::kTile));            // S(j + 2) over dS(j)
             commit(L::S_FULL + b);
           }
@@ -506,8 +485,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_bwd_q_kernel(const __grid_co
           s = s == kKStages - 1 ? 0 : s + 1;
           r = r == 0 ? 2 : r - 1;                             // 2 (j + 1) % 3
         }
-        if (lane == 0)
-          for (int i = max(0, done - kKStages); i < done; ++i)
+        for (int i = max(0, done - kKStages); i < done; ++i)
             mbar_drain(bar(L::K_EMPTY + i % kKStages), (i / kKStages) & 1);
       }
     }
@@ -565,7 +543,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_bwd_q_kernel(const __grid_co
       mbar_arrive(bar(L::DS_FULL + (j & 1)));
     }
     // each warpgroup stores half of dQ's columns
-    __nv_bfloat16* out = static_cast<__nv_bfloat16*>(prm.out0) + at * D + x * (D / 2);
+    __nv_bfloat16* out = static_cast<__nv_bfloat16*>(prm.dq) + at * D + x * (D / 2);
     if (n_tiles == 0) {
       if (row_ok)
         for (int c = 0; c < D / 16; ++c) reinterpret_cast<uint4*>(out)[c] = make_uint4(0, 0, 0, 0);
@@ -583,19 +561,25 @@ __global__ void __launch_bounds__(kThreads, 1) attn_bwd_q_kernel(const __grid_co
   }
 }
 
+// One launch: the CTAs of the dK, dV kernel first, those of dQ behind them, each longest first (the
+// hardware hands them out in order), so that there is one tail instead of two.
 template <int D>
-int kv_impl(const BwdTcParams& prm, int units, cudaStream_t st) {
-  cudaError_t e = cudaFuncSetAttribute(attn_bwd_kv_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, KvLayout<D>::kBytes);
-  if (e != cudaSuccess) return static_cast<int>(e);
-  attn_bwd_kv_kernel<D><<<units, kThreads, KvLayout<D>::kBytes, st>>>(prm);
-  return static_cast<int>(cudaGetLastError());
+__global__ void __launch_bounds__(kThreads, 1) attn_bwd_tc_kernel(const __grid_constant__ BwdTcParams prm) {
+  extern __shared__ __align__(1024) uint8_t smem[];
+  const uint32_t base = smem_u32(smem);
+  if (!smem_aligned(base, prm.status)) return;
+  if (static_cast<int>(blockIdx.x) < prm.kv.units)
+    dkdv_unit<D>(prm, blockIdx.x, smem, base);
+  else
+    dq_unit<D>(prm, blockIdx.x - prm.kv.units, smem, base);
 }
 
 template <int D>
-int q_impl(const BwdTcParams& prm, int units, cudaStream_t st) {
-  cudaError_t e = cudaFuncSetAttribute(attn_bwd_q_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, QLayout<D>::kBytes);
+int tc_impl(const BwdTcParams& prm, cudaStream_t st) {
+  constexpr int smem = KvLayout<D>::kBytes > QLayout<D>::kBytes ? KvLayout<D>::kBytes : QLayout<D>::kBytes;
+  cudaError_t e = cudaFuncSetAttribute(attn_bwd_tc_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return static_cast<int>(e);
-  attn_bwd_q_kernel<D><<<units, kThreads, QLayout<D>::kBytes, st>>>(prm);
+  attn_bwd_tc_kernel<D><<<prm.kv.units + prm.q.units, kThreads, smem, st>>>(prm);
   return static_cast<int>(cudaGetLastError());
 }
 
@@ -603,12 +587,8 @@ int q_impl(const BwdTcParams& prm, int units, cudaStream_t st) {
 
 int attn_bwd_tc_tile_rows() { return kRows; }
 
-int launch_attn_bwd_kv(const BwdTcParams& prm, int D, int units, cudaStream_t st) {
-  return D == 64 ? kv_impl<64>(prm, units, st) : kv_impl<128>(prm, units, st);
-}
-
-int launch_attn_bwd_q(const BwdTcParams& prm, int D, int units, cudaStream_t st) {
-  return D == 64 ? q_impl<64>(prm, units, st) : q_impl<128>(prm, units, st);
+int launch_attn_bwd_tc(const BwdTcParams& prm, int D, cudaStream_t st) {
+  return D == 64 ? tc_impl<64>(prm, st) : tc_impl<128>(prm, st);
 }
 
 }  // namespace pa

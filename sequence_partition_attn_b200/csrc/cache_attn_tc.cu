@@ -85,19 +85,6 @@ __device__ __forceinline__ void weights_half(const float (&s)[kBN], float m, flo
   }
 }
 
-// O_x (+)= P_x V over keys 64 H .. 64 H + 63: P's pairs are 32 consecutive TMEM columns per half.
-template <int D, int H>
-__device__ __forceinline__ void product_pv(uint32_t o_tmem, uint32_t p_tmem, uint64_t v, bool first) {
-  constexpr uint32_t id = idesc_bf16(kBM, D, false, true);
-#pragma unroll
-  for (int kk = H * 4; kk < H * 4 + 4; ++kk) {
-    if (elect_one())
-      tiles::mma_ts(o_tmem, p_tmem + kk * 8, v + static_cast<uint32_t>((kk * 16 * 128) >> 4), id,
-                    (first && kk == 0) ? 0u : 1u);
-    __syncwarp();
-  }
-}
-
 // Four codes times a power of two, as bf16 pairs.
 __device__ __forceinline__ void widen(uint32_t codes, float2 scale, uint32_t& lo, uint32_t& hi) {
   uint32_t h[2];
@@ -201,15 +188,12 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attn_tc_kernel(const __grid
           tiles::load_tile<D>(base + L::kQ + x * L::kTile, &p.tm_q, row0 + x * kBM, bh, bar(L::Q_FULL));
         mbar_drain(bar(L::Q_FULL), 0);
       }
-    } else if (warp == 1 && T > 0) {
+    } else if (warp == 1 && T > 0 && elect_one()) {
       // ---------------------------------------------------------------- MMA issuer
       // Per tile j: PV_a(j), S_a(j+1), PV_b(j), S_b(j+1); S_x(j+1) overwrites the P_x(j) that the
       // product issued before it reads.
-      auto wait = [&](int b, uint32_t parity) { return mbar_wait_warp(bar(b), parity, abort_flag, status); };
-      auto commit = [&](int b) {
-        if (elect_one()) mma_commit(bar(b));
-        __syncwarp();
-      };
+      auto wait = [&](int b, uint32_t parity) { return mbar_wait(bar(b), parity, abort_flag, status); };
+      auto commit = [&](int b) { mma_commit(bar(b)); };
       const uint64_t dq[2] = {tiles::kmajor(base + L::kQ), tiles::kmajor(base + L::kQ + L::kTile)};
       bool ok = wait(L::Q_FULL, 0) && wait(L::K_FULL, 0) && wait(L::V_FULL, 0);
       if (ok) {
@@ -230,13 +214,13 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attn_tc_kernel(const __grid
           const uint32_t tP = tmem + x * 128, tO = tmem + 256 + x * 128;
           if (!(ok = wait(L::P_LO + x, j & 1))) break;
           tc_fence_after();
-          product_pv<D, 0>(tO, tP, dv, j == 0);
+          tiles::product_w<D, 32, 0x0F>(tO, tP, dv, j == 0);
           // the next operands are checked while P's second half is still being produced
           if (more && !(ok = x == 0 ? wait(L::K_FULL + s1, ph1) : true)) break;
           if (more && x == nx - 1 && !(ok = wait(L::V_FULL + s1, ph1))) break;
           if (!(ok = wait(L::P_HI + x, j & 1))) break;
           tc_fence_after();
-          product_pv<D, 1>(tO, tP, dv, j == 0);
+          tiles::product_w<D, 32, 0xF0>(tO, tP, dv, false);
           if (!more) commit(L::O_FINAL + x);
           if (x == nx - 1) commit(L::V_EMPTY + s);
           if (more) {
@@ -247,11 +231,10 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attn_tc_kernel(const __grid
         }
         if (ok) ++done;
       }
-      if (lane == 0)                     // the last commits arrive before the CTA exits
-        for (int i = max(0, done - kStages); i < done; ++i) {
-          mbar_drain(bar(L::K_EMPTY + i % kStages), (i / kStages) & 1);
-          mbar_drain(bar(L::V_EMPTY + i % kStages), (i / kStages) & 1);
-        }
+      for (int i = max(0, done - kStages); i < done; ++i) {   // the last commits arrive before the CTA exits
+        mbar_drain(bar(L::K_EMPTY + i % kStages), (i / kStages) & 1);
+        mbar_drain(bar(L::V_EMPTY + i % kStages), (i / kStages) & 1);
+      }
     }
   } else if (warp < 12) {
     // ---------------------------------------------------------------- softmax

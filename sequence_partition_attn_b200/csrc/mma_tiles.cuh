@@ -61,16 +61,16 @@ __device__ __forceinline__ void load_tile(uint32_t dst, const CUtensorMap* m, in
   for (int a = 0; a < D / 64; ++a) tma_load_3d(dst + a * kAtomBytes, m, a * 64, row, bh, bar);
 }
 
-// Zero rows [from, 128) of a tile (one whole warp, which then issues the products that read it).
-// A row of an atom is 128 contiguous bytes whatever the swizzle.
+// Zero rows [from, 128) of a tile (the thread that then issues the products that read it).  A row
+// of an atom is 128 contiguous bytes whatever the swizzle.
 template <int D>
-__device__ __forceinline__ void zero_rows(uint8_t* tile, int from, int lane) {
-  for (int i = lane; i < (kRows - from) * (D / 64) * 8; i += 32) {
+__device__ __forceinline__ void zero_rows(uint8_t* tile, int from) {
+#pragma unroll 1
+  for (int i = 0; i < (kRows - from) * (D / 64) * 8; ++i) {
     const int c = i % 8, r = from + i / 8 % (kRows - from), a = i / 8 / (kRows - from);
     *reinterpret_cast<uint4*>(tile + a * kAtomBytes + r * 128 + c * 16) = make_uint4(0u, 0u, 0u, 0u);
   }
   fence_async_smem();
-  __syncwarp();
 }
 
 // D[tmem] (+)= A[tmem] * B[smem desc]; A (128 x 16 bf16) is read from 8 TMEM columns.
@@ -87,30 +87,30 @@ __device__ __forceinline__ void mma_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_
 __device__ __forceinline__ uint64_t kmajor(uint32_t smem) { return smem_desc_sw128(smem, 16, 1024); }
 __device__ __forceinline__ uint64_t mnmajor(uint32_t smem) { return smem_desc_sw128(smem, kAtomBytes, 1024); }
 
-// C[128 x 128] = A B^T over D: both tiles K-major.  Whole warp, one elected lane issues.
+// C[128 x 128] = A B^T over D: both tiles K-major.
 template <int D>
 __device__ __forceinline__ void product_nt(uint32_t c_tmem, uint64_t a, uint64_t b) {
   constexpr uint32_t id = idesc_bf16(kRows, kRows, false, false);
 #pragma unroll
   for (int kk = 0; kk < D / 16; ++kk) {
     const uint32_t off = static_cast<uint32_t>(((kk >> 2) * kAtomBytes + (kk & 3) * 32) >> 4);
-    if (elect_one()) mma_bf16_ss(c_tmem, a + off, b + off, id, kk > 0);
-    __syncwarp();
+    mma_bf16_ss(c_tmem, a + off, b + off, id, kk > 0);
   }
 }
 
 // C[128 x D] (+)= W B over 128 rows of B (MN-major).  W is 128 x 128 bf16 in TMEM, its columns
-// 0-63 (as pairs) at w_tmem and 64-127 at w_tmem + 64: the places its two writers read from.
-template <int D>
+// 0-63 (as pairs) at w_tmem and 64-127 at w_tmem + kSecond.  kSteps: which k-steps of 16 rows, a
+// bit each; `first` overwrites C with the first of them.
+template <int D, int kSecond, uint32_t kSteps = 0xFF>
 __device__ __forceinline__ void product_w(uint32_t c_tmem, uint32_t w_tmem, uint64_t b, bool first) {
   constexpr uint32_t id = idesc_bf16(kRows, D, false, true);
+  uint32_t acc = first ? 0u : 1u;
 #pragma unroll
-  for (int kk = 0; kk < 8; ++kk) {
-    if (elect_one())
-      mma_ts(c_tmem, w_tmem + (kk >> 2) * 64 + (kk & 3) * 8, b + static_cast<uint32_t>((kk * 16 * 128) >> 4), id,
-             (first && kk == 0) ? 0u : 1u);
-    __syncwarp();
-  }
+  for (int kk = 0; kk < 8; ++kk)
+    if (kSteps >> kk & 1) {
+      mma_ts(c_tmem, w_tmem + (kk >> 2) * kSecond + (kk & 3) * 8, b + static_cast<uint32_t>((kk * 16 * 128) >> 4), id, acc);
+      acc = 1u;
+    }
 }
 
 // 128 x D fp32 accumulator rows (one per thread) times `f`, as bf16 to global memory.

@@ -697,6 +697,32 @@ static int fill_owner_tiles(pa::AttnTables& t, int tile_rows) {
   return acc;
 }
 
+// Launch order of the bf16 backward pass's units: groups that stream the most tokens first (ties in
+// group order), all heads and tiles of a group together, which share what they stream.
+static bool fill_units(pa::BwdSide& side, long long BH) {
+  const pa::AttnTables& t = side.t;
+  const int tile = pa::attn_bwd_tc_tile_rows();
+  long long tokens[PA_MAX_P];
+  for (int g = 0; g < t.QG; ++g) {
+    tokens[g] = 0;
+    for (int p = 0; p < t.P; ++p)
+      if (pa::fresh_bit(t.fresh_bits, g, p)) tokens[g] += t.part_off[p + 1] - t.part_off[p];
+    int i = g;
+    for (; i > 0 && tokens[side.order[i - 1]] < tokens[g]; --i) side.order[i] = side.order[i - 1];
+    side.order[i] = static_cast<uint8_t>(g);
+  }
+  long long acc = 0;
+  for (int i = 0; i < t.QG; ++i) {
+    const int g = side.order[i];
+    side.unit_start[i] = static_cast<int>(acc);
+    acc += (t.qg_row0[g + 1] - t.qg_row0[g] + tile - 1) / tile * BH;
+    if (acc > 0x7fffffffLL) return false;
+  }
+  side.unit_start[t.QG] = static_cast<int>(acc);
+  side.units = static_cast<int>(acc);
+  return true;
+}
+
 static int pa_attn_backward_impl(pa_ctx* ctx, const pa_attn_bwd_desc* d, void* stream) {
   if (!ctx) return fail(nullptr, PA_EINVAL, "ctx is NULL");
   if (!d) return fail(ctx, PA_EINVAL, "desc is NULL");
@@ -706,9 +732,8 @@ static int pa_attn_backward_impl(pa_ctx* ctx, const pa_attn_bwd_desc* d, void* s
   const long long BH = static_cast<long long>(d->B) * d->H;
   if (BH > 65535) return fail(ctx, PA_EINVAL, "B*H=%lld exceeds 65535", BH);
   if (!(d->scale > 0.0f) || !(d->scale < 1e30f)) return fail(ctx, PA_EINVAL, "scale must be positive and finite");
-  pa::BwdParams prm;
-  memset(&prm, 0, sizeof prm);
-  int rc = build_tables(ctx, d->N, d->P, d->G, d->part_off, d->fresh, prm.tq);
+  pa::AttnTables tq;
+  int rc = build_tables(ctx, d->N, d->P, d->G, d->part_off, d->fresh, tq);
   if (rc) return rc;
   if (d->N == 0) return PA_OK;
   if (!d->q || !d->k || !d->v || !d->o || !d->lse || !d->dout || !d->dq || !d->dk || !d->dv || !d->delta)
@@ -718,68 +743,66 @@ static int pa_attn_backward_impl(pa_ctx* ctx, const pa_attn_bwd_desc* d, void* s
     return fail(ctx, PA_EALIGN, "q, k, v, o and the gradients must be 16-byte aligned");
   if (!aligned(d->lse, 4) || !aligned(d->delta, 4) || (d->dlse && !aligned(d->dlse, 4)))
     return fail(ctx, PA_EALIGN, "lse, dlse and delta must be 4-byte aligned");
-  if ((rc = check_device(ctx))) return rc;
-  // The same table with keys as owners: KV group g streams the query partitions it is fresh for.
-  prm.tk = prm.tq;
-  memset(prm.tk.fresh_bits, 0, sizeof prm.tk.fresh_bits);
-  for (int p = 0; p < d->P; ++p)
-    for (int kg = 0; kg < prm.tq.QG; ++kg)
-      if (!d->fresh || d->fresh[(p / d->G) * prm.tq.QG + kg]) prm.tk.fresh_bits[kg][p >> 5] |= 1u << (p & 31);
-  merge_equal_groups(prm.tq);
-  merge_equal_groups(prm.tk);
-  cudaStream_t st = static_cast<cudaStream_t>(stream);
-  prm.q = d->q;
-  prm.k = d->k;
-  prm.v = d->v;
-  prm.dout = d->dout;
-  prm.lse = d->lse;
-  prm.delta = d->delta;
-  prm.dq = d->dq;
-  prm.dk = d->dk;
-  prm.dv = d->dv;
-  prm.BH = (int)BH;
-  prm.N = d->N;
-  prm.D = d->D;
-  prm.scale = d->scale;
   const long long rows = BH * d->N;
   if (rows > 0x7fffffffLL * 8) return fail(ctx, PA_EINVAL, "too many rows");
-  const int tile = d->dtype == PA_BF16 ? pa::attn_bwd_tc_tile_rows() : pa::attn_bwd_fma_tile_rows();
-  prm.tiles_q = fill_owner_tiles(prm.tq, tile);
-  prm.tiles_k = fill_owner_tiles(prm.tk, tile);
-  const long long units = BH * std::max(prm.tiles_q, prm.tiles_k);
-  if (units > 0x7fffffffLL) return fail(ctx, PA_EINVAL, "too many work units");
-  pa::BwdTcParams tc;
-  if (d->dtype == PA_BF16) {
-    memset(&tc, 0, sizeof tc);
-    if ((rc = encode_qkv_map(ctx, &tc.tm_q, d->q, (int)BH, d->N, d->D))) return rc;
-    if ((rc = encode_qkv_map(ctx, &tc.tm_k, d->k, (int)BH, d->N, d->D))) return rc;
-    if ((rc = encode_qkv_map(ctx, &tc.tm_v, d->v, (int)BH, d->N, d->D))) return rc;
-    if ((rc = encode_qkv_map(ctx, &tc.tm_do, d->dout, (int)BH, d->N, d->D))) return rc;
-  }
-  int e = pa::launch_delta(d->o, d->dout, d->dlse, d->delta, rows, d->D, d->dtype, st);
-  if (e) return cuda_fail(ctx, e, "delta launch");
+  if ((rc = check_device(ctx))) return rc;
+  // The same table with keys as owners: KV group g streams the query partitions it is fresh for.
+  pa::AttnTables tk = tq;
+  memset(tk.fresh_bits, 0, sizeof tk.fresh_bits);
+  for (int p = 0; p < d->P; ++p)
+    for (int kg = 0; kg < tq.QG; ++kg)
+      if (!d->fresh || d->fresh[(p / d->G) * tq.QG + kg]) tk.fresh_bits[kg][p >> 5] |= 1u << (p & 31);
+  merge_equal_groups(tq);
+  merge_equal_groups(tk);
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  int e = 0;
   if (d->dtype == PA_F32) {
+    pa::BwdParams prm;
+    memset(&prm, 0, sizeof prm);
+    prm.tq = tq;
+    prm.tk = tk;
+    prm.q = d->q;
+    prm.k = d->k;
+    prm.v = d->v;
+    prm.dout = d->dout;
+    prm.lse = d->lse;
+    prm.delta = d->delta;
+    prm.dq = d->dq;
+    prm.dk = d->dk;
+    prm.dv = d->dv;
+    prm.BH = (int)BH;
+    prm.N = d->N;
+    prm.D = d->D;
+    prm.scale = d->scale;
+    prm.tiles_q = fill_owner_tiles(prm.tq, pa::attn_bwd_fma_tile_rows());
+    prm.tiles_k = fill_owner_tiles(prm.tk, pa::attn_bwd_fma_tile_rows());
+    e = pa::launch_delta(d->o, d->dout, d->dlse, d->delta, rows, d->D, d->dtype, st);
+    if (e) return cuda_fail(ctx, e, "delta launch");
     e = pa::launch_attn_bwd_fma(prm, st);
     return e ? cuda_fail(ctx, e, "attention backward launch") : PA_OK;
   }
+  pa::BwdTcParams tc;
+  if ((rc = encode_qkv_map(ctx, &tc.tm_q, d->q, (int)BH, d->N, d->D))) return rc;
+  if ((rc = encode_qkv_map(ctx, &tc.tm_k, d->k, (int)BH, d->N, d->D))) return rc;
+  if ((rc = encode_qkv_map(ctx, &tc.tm_v, d->v, (int)BH, d->N, d->D))) return rc;
+  if ((rc = encode_qkv_map(ctx, &tc.tm_do, d->dout, (int)BH, d->N, d->D))) return rc;
   tc.lse = d->lse;
   tc.delta = d->delta;
+  tc.dq = d->dq;
+  tc.dk = d->dk;
+  tc.dv = d->dv;
   tc.status = ctx->d_status;
   tc.N = d->N;
   tc.scale = d->scale;
   tc.scale_log2 = d->scale * 1.4426950408889634f;
-  tc.t = prm.tk;
-  tc.tiles_total = prm.tiles_k;
-  tc.out0 = d->dk;
-  tc.out1 = d->dv;
-  e = pa::launch_attn_bwd_kv(tc, d->D, static_cast<int>(BH * prm.tiles_k), st);
-  if (e) return cuda_fail(ctx, e, "attention backward (dK, dV) launch");
-  tc.t = prm.tq;
-  tc.tiles_total = prm.tiles_q;
-  tc.out0 = d->dq;
-  tc.out1 = nullptr;
-  e = pa::launch_attn_bwd_q(tc, d->D, static_cast<int>(BH * prm.tiles_q), st);
-  return e ? cuda_fail(ctx, e, "attention backward (dQ) launch") : PA_OK;
+  tc.kv.t = tk;
+  tc.q.t = tq;
+  if (!fill_units(tc.kv, BH) || !fill_units(tc.q, BH) || tc.kv.units > 0x7fffffff - tc.q.units)
+    return fail(ctx, PA_EINVAL, "too many work units");
+  e = pa::launch_delta(d->o, d->dout, d->dlse, d->delta, rows, d->D, d->dtype, st);
+  if (e) return cuda_fail(ctx, e, "delta launch");
+  e = pa::launch_attn_bwd_tc(tc, d->D, st);
+  return e ? cuda_fail(ctx, e, "attention backward launch") : PA_OK;
 }
 
 static int pa_cache_store_impl(pa_ctx* ctx, const pa_cache_store_desc* d, void* stream) {

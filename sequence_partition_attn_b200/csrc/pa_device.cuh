@@ -381,17 +381,26 @@ struct BwdParams {
   AttnTables tq, tk;
 };
 
-// One of the two bf16 kernels: t holds its owner groups and the partitions they stream.
+// Owners of row tiles in the bf16 backward pass: their groups with the partitions they stream, and
+// the launch order of the units (group, head, tile): groups with the most to stream first.
+struct BwdSide {
+  AttnTables t;
+  int units;
+  int unit_start[PA_MAX_P + 1];   // by place in the order
+  uint8_t order[PA_MAX_P];
+};
+
 struct BwdTcParams {
   CUtensorMap tm_q, tm_k, tm_v, tm_do;
   const float* lse;
   const float* delta;
-  void* out0;                     // dK | dQ
-  void* out1;                     // dV
+  void* dq;
+  void* dk;
+  void* dv;
   int* status;
-  int N, tiles_total;
+  int N;
   float scale, scale_log2;
-  AttnTables t;
+  BwdSide kv, q;
 };
 
 struct CacheStoreParams {

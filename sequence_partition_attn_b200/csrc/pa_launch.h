@@ -40,8 +40,7 @@ int attn_bwd_fma_tile_rows();
 int launch_attn_bwd_fma(const BwdParams& prm, cudaStream_t st);
 
 int attn_bwd_tc_tile_rows();
-int launch_attn_bwd_kv(const BwdTcParams& prm, int D, int units, cudaStream_t st);
-int launch_attn_bwd_q(const BwdTcParams& prm, int D, int units, cudaStream_t st);
+int launch_attn_bwd_tc(const BwdTcParams& prm, int D, cudaStream_t st);
 
 int launch_cache_store(const CacheStoreParams& prm, unsigned blocks, int dtype, int D, cudaStream_t st);
 
