@@ -49,176 +49,240 @@ __global__ void __launch_bounds__(256) delta_kernel(const T* __restrict__ o, con
 }
 
 // ------------------------------------------------------------------ FMA kernels
-constexpr int kT = 64;               // rows and keys per tile
-constexpr int kThreads = 256;        // 16 x 16: four rows by four keys each
+// A block owns kOwn rows (queries for dQ, keys for dK and dV) and streams tiles of 64 rows of the
+// other side through shared memory.  Products run on packed pairs of fp32 (two multiply-adds per
+// instruction: the multiply-add pipe, not the issue slots, is then what bounds them); pairs run
+// along the summed index in the first products and along the channels in the second.
+constexpr int kT = 64;               // streamed rows per tile
+constexpr int kThreads = 256;        // 16 x 16
 
-template <int D>
+template <int D, int kOwn>
 struct Smem {
-  static constexpr int kRow = D + 4;     // 16-byte reads of 8 rows then fall in different banks
-  static constexpr int kPRow = kT + 4;
+  static constexpr int kRow = D + 4;       // 16-byte reads of 8 rows then fall in different banks
+  static constexpr int kOwnTile = kOwn * kRow;
   static constexpr int kTile = kT * kRow;
+  static constexpr int kPRow = kOwn + 4;   // weights [streamed row][own row]
   static constexpr int kP = kT * kPRow;
-  static constexpr int kBytes = (4 * kTile + 2 * kP + 2 * kT) * 4;
+  static constexpr int kBytes = (2 * kOwnTile + 2 * kTile + 2 * kP + 2 * kT) * 4;
 };
 
-// Rows [r0, r0 + 64) of a [.., D] tensor into shared memory; rows at or past `end` read as 0,
+// Rows [r0, r0 + kRows) of a [.., D] tensor into shared memory; rows at or past `end` read as 0,
 // so that nothing outside the range (which may be non-finite) reaches a product.
-template <int D>
+template <int D, int kRows>
 __device__ __forceinline__ void load_tile(float* dst, const float* src, int r0, int end) {
-  for (int i = threadIdx.x; i < kT * D / 4; i += kThreads) {
+#pragma unroll 4
+  for (int i = threadIdx.x; i < kRows * D / 4; i += kThreads) {
     const int r = i / (D / 4), c = (i % (D / 4)) * 4;
     const float4 v = r0 + r < end ? load4(src + static_cast<size_t>(r0 + r) * D + c) : make_float4(0.f, 0.f, 0.f, 0.f);
-    *reinterpret_cast<float4*>(dst + r * Smem<D>::kRow + c) = v;
+    *reinterpret_cast<float4*>(dst + r * (D + 4) + c) = v;
   }
 }
 
-// acc[i][j] = a[4 ty + i] . b[tx + 16 j]
+// The same tile in two steps: into registers, while the one before is used, and on to shared memory.
 template <int D>
-__device__ __forceinline__ void dot_tile(float (&acc)[4][4], const float* a, const float* b, int ty, int tx) {
+struct Ahead {
+  static constexpr int kN = kT * D / 4 / kThreads;
+  float4 v[kN];
+  __device__ __forceinline__ void load(const float* src, int r0, int end) {
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
+    for (int n = 0; n < kN; ++n) {
+      const int i = n * kThreads + threadIdx.x;
+      const int r = r0 + i / (D / 4);
+      v[n] = r < end ? load4(src + static_cast<size_t>(r) * D + (i % (D / 4)) * 4) : make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+  }
+  __device__ __forceinline__ void store(float* dst) const {
 #pragma unroll
-    for (int j = 0; j < 4; ++j) acc[i][j] = 0.0f;
+    for (int n = 0; n < kN; ++n) {
+      const int i = n * kThreads + threadIdx.x;
+      *reinterpret_cast<float4*>(dst + i / (D / 4) * (D + 4) + (i % (D / 4)) * 4) = v[n];
+    }
+  }
+};
+
+// acc[i][j] = a[RA ty + i] . b[tx + 16 j]
+template <int D, int RA, int RB>
+__device__ __forceinline__ void dot_tile(float (&acc)[RA][RB], const float* a, const float* b, int ty, int tx) {
+  float2 sum[RA][RB];
+#pragma unroll
+  for (int i = 0; i < RA; ++i)
+#pragma unroll
+    for (int j = 0; j < RB; ++j) sum[i][j] = make_float2(0.0f, 0.0f);
 #pragma unroll 4
   for (int d = 0; d < D; d += 4) {
-    float4 x[4], y[4];
+    float4 x[RA], y[RB];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) x[i] = *reinterpret_cast<const float4*>(a + (4 * ty + i) * Smem<D>::kRow + d);
+    for (int i = 0; i < RA; ++i) x[i] = *reinterpret_cast<const float4*>(a + (RA * ty + i) * (D + 4) + d);
 #pragma unroll
-    for (int j = 0; j < 4; ++j) y[j] = *reinterpret_cast<const float4*>(b + (tx + 16 * j) * Smem<D>::kRow + d);
+    for (int j = 0; j < RB; ++j) y[j] = *reinterpret_cast<const float4*>(b + (tx + 16 * j) * (D + 4) + d);
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
+    for (int i = 0; i < RA; ++i)
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        acc[i][j] = fmaf(x[i].x, y[j].x, acc[i][j]);
-        acc[i][j] = fmaf(x[i].y, y[j].y, acc[i][j]);
-        acc[i][j] = fmaf(x[i].z, y[j].z, acc[i][j]);
-        acc[i][j] = fmaf(x[i].w, y[j].w, acc[i][j]);
+      for (int j = 0; j < RB; ++j) {
+        sum[i][j] = __ffma2_rn(make_float2(x[i].x, x[i].y), make_float2(y[j].x, y[j].y), sum[i][j]);
+        sum[i][j] = __ffma2_rn(make_float2(x[i].z, x[i].w), make_float2(y[j].z, y[j].w), sum[i][j]);
       }
   }
+#pragma unroll
+  for (int i = 0; i < RA; ++i)
+#pragma unroll
+    for (int j = 0; j < RB; ++j) acc[i][j] = sum[i][j].x + sum[i][j].y;
 }
 
-// acc[i][c] += sum_t w[t][4 ty + i] * x[t][4 tx + 64 (c / 4) + c % 4]
-template <int D>
-__device__ __forceinline__ void add_product(float (&acc)[4][D / 16], const float* w, const float* x, int ty, int tx) {
+// acc[i][2 c + e] += sum_t w[t][RO ty + i] * x[t][4 tx + 64 c + 2 e ..] (pairs of channels)
+template <int D, int RO>
+__device__ __forceinline__ void add_product(float2 (&acc)[RO][D / 32], const float* w, const float* x, int ty, int tx) {
 #pragma unroll 4
   for (int t = 0; t < kT; ++t) {
-    const float4 a = *reinterpret_cast<const float4*>(w + t * Smem<D>::kPRow + 4 * ty);
-    const float av[4] = {a.x, a.y, a.z, a.w};
+    float a[RO];
+#pragma unroll
+    for (int i = 0; i < RO; i += 2) {
+      const float2 p = *reinterpret_cast<const float2*>(w + t * (16 * RO + 4) + RO * ty + i);
+      a[i] = p.x;
+      a[i + 1] = p.y;
+    }
 #pragma unroll
     for (int c = 0; c < D / 64; ++c) {
-      const float4 b = *reinterpret_cast<const float4*>(x + t * Smem<D>::kRow + 4 * tx + 64 * c);
+      const float4 b = *reinterpret_cast<const float4*>(x + t * (D + 4) + 4 * tx + 64 * c);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        acc[i][4 * c] = fmaf(av[i], b.x, acc[i][4 * c]);
-        acc[i][4 * c + 1] = fmaf(av[i], b.y, acc[i][4 * c + 1]);
-        acc[i][4 * c + 2] = fmaf(av[i], b.z, acc[i][4 * c + 2]);
-        acc[i][4 * c + 3] = fmaf(av[i], b.w, acc[i][4 * c + 3]);
+      for (int i = 0; i < RO; ++i) {
+        acc[i][2 * c] = __ffma2_rn(make_float2(a[i], a[i]), make_float2(b.x, b.y), acc[i][2 * c]);
+        acc[i][2 * c + 1] = __ffma2_rn(make_float2(a[i], a[i]), make_float2(b.z, b.w), acc[i][2 * c + 1]);
       }
     }
   }
 }
 
-// kDq: the block owns 64 query rows and streams keys; else it owns 64 keys and streams queries.
-// Four rows by four keys per thread: 8 shared 16-byte reads per 64 multiply-adds, which is what
-// bounds it (shared memory reads at twice the rate the FMA pipe would need).
-template <int D, bool kDq>
-__global__ void __launch_bounds__(kThreads) attn_bwd_fma_kernel(const __grid_constant__ BwdParams prm) {
-  extern __shared__ __align__(16) float smem[];
-  float* sQ = smem;
-  float* sdO = sQ + Smem<D>::kTile;
-  float* sK = sdO + Smem<D>::kTile;
-  float* sV = sK + Smem<D>::kTile;
-  float* sP = sV + Smem<D>::kTile;         // dS^T [key][row] for dQ; P [row][key] for dV
-  float* sdS = sP + Smem<D>::kP;           // dS [row][key] for dK
-  float* sLse = sdS + Smem<D>::kP;
+template <int D, int RO>
+__device__ __forceinline__ void store_tile(float* dst, const float2 (&acc)[RO][D / 32], float f, int own0, int own1, int ty, int tx) {
+#pragma unroll
+  for (int i = 0; i < RO; ++i) {
+    const int r = own0 + RO * ty + i;
+    if (r >= own1) continue;
+#pragma unroll
+    for (int c = 0; c < D / 64; ++c)
+      store4(dst + static_cast<size_t>(r) * D + 4 * tx + 64 * c,
+             make_float4(acc[i][2 * c].x * f, acc[i][2 * c].y * f, acc[i][2 * c + 1].x * f, acc[i][2 * c + 1].y * f));
+  }
+}
+
+// kDq: the block owns queries and streams keys; else it owns keys and streams queries.
+template <int D, int kOwn, bool kDq>
+__device__ __forceinline__ void fma_unit(const BwdParams& prm, int tile, float* smem) {
+  using S = Smem<D, kOwn>;
+  constexpr int RO = kOwn / 16;                      // own rows per thread
+  constexpr int RA = kDq ? RO : kT / 16, RB = kDq ? kT / 16 : RO;
+  float* sOwn0 = smem;                               // Q | K
+  float* sOwn1 = sOwn0 + S::kOwnTile;                // dO | V
+  float* sStr0 = sOwn1 + S::kOwnTile;                // K | Q
+  float* sStr1 = sStr0 + S::kTile;                   // V | dO
+  float* sP = sStr1 + S::kTile;                      // dS | P, by streamed row
+  float* sdS = sP + S::kP;                           //      dS
+  float* sLse = sdS + S::kP;
   float* sDelta = sLse + kT;
   const AttnTables& t = kDq ? prm.tq : prm.tk;
   const int bh = blockIdx.y;
-  const int ty = threadIdx.x / 16, tx = threadIdx.x % 16;
+  // A warp covers 4 x 8 of the 16 x 16 threads.
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int ty = (warp >> 1) * 4 + (lane >> 3), tx = (warp & 1) * 8 + (lane & 7);
   int g = 0;
-  while (g + 1 < t.QG && t.tile_start[g + 1] <= static_cast<int>(blockIdx.x)) ++g;
-  const int own0 = t.qg_row0[g] + (blockIdx.x - t.tile_start[g]) * kT;
-  const int own1 = min(own0 + kT, t.qg_row0[g + 1]);
+  while (g + 1 < t.QG && t.tile_start[g + 1] <= tile) ++g;
+  const int own0 = t.qg_row0[g] + (tile - t.tile_start[g]) * kOwn;
+  const int own1 = min(own0 + kOwn, t.qg_row0[g + 1]);
   const size_t head = static_cast<size_t>(bh) * prm.N;
   const float* q = static_cast<const float*>(prm.q) + head * D;
   const float* k = static_cast<const float*>(prm.k) + head * D;
   const float* v = static_cast<const float*>(prm.v) + head * D;
   const float* dout = static_cast<const float*>(prm.dout) + head * D;
+  // +inf makes every P of the row 0: rows outside the range, and rows without any key
+  auto load_stats = [&](int r0, int r1, int n) {
+    if (static_cast<int>(threadIdx.x) < n) {
+      const int r = r0 + threadIdx.x;
+      const float l = r < r1 ? prm.lse[head + r] : INFINITY;
+      sLse[threadIdx.x] = l == -INFINITY ? INFINITY : l;
+      sDelta[threadIdx.x] = r < r1 ? prm.delta[head + r] : 0.0f;
+    }
+  };
+  load_tile<D, kOwn>(sOwn0, kDq ? q : k, own0, own1);
+  load_tile<D, kOwn>(sOwn1, kDq ? dout : v, own0, own1);
+  if (kDq) load_stats(own0, own1, kOwn);
 
-  float acc0[4][D / 16] = {}, acc1[4][D / 16] = {};      // dQ | dK, dV
-  for (int p = 0; p < t.P;) {
-    int s0, s1;
-    p = next_range(t, g, p, s0, s1);
-    for (int st0 = s0; st0 < s1; st0 += kT) {
-      const int q0 = kDq ? own0 : st0, q1 = kDq ? own1 : s1;
-      const int k0 = kDq ? st0 : own0, k1 = kDq ? s1 : own1;
-      __syncthreads();
-      load_tile<D>(sQ, q, q0, q1);
-      load_tile<D>(sdO, dout, q0, q1);
-      load_tile<D>(sK, k, k0, k1);
-      load_tile<D>(sV, v, k0, k1);
-      if (threadIdx.x < kT) {
-        const int r = q0 + threadIdx.x;
-        // +inf makes every P of the row 0: rows outside the range, and rows without any key
-        const float l = r < q1 ? prm.lse[head + r] : INFINITY;
-        sLse[threadIdx.x] = l == -INFINITY ? INFINITY : l;
-        sDelta[threadIdx.x] = r < q1 ? prm.delta[head + r] : 0.0f;
-      }
-      __syncthreads();
-      float s[4][4], dp[4][4];
-      dot_tile<D>(s, sQ, sK, ty, tx);
-      dot_tile<D>(dp, sdO, sV, ty, tx);
+  float2 acc0[RO][D / 32], acc1[RO][D / 32];         // dQ | dK, dV
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
+  for (int i = 0; i < RO; ++i)
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const int r = 4 * ty + i, c = tx + 16 * j;
-          const bool in = q0 + r < q1 && k0 + c < k1;
-          const float pij = in ? expf(fmaf(s[i][j], prm.scale, -sLse[r])) : 0.0f;
-          const float ds = in ? pij * (dp[i][j] - sDelta[r]) : 0.0f;
-          if (kDq) {
-            sP[c * Smem<D>::kPRow + r] = ds;
-          } else {
-            sP[r * Smem<D>::kPRow + c] = pij;
-            sdS[r * Smem<D>::kPRow + c] = ds;
-          }
+    for (int c = 0; c < D / 32; ++c) acc0[i][c] = acc1[i][c] = make_float2(0.0f, 0.0f);
+  const float* str0 = kDq ? k : q;
+  const float* str1 = kDq ? v : dout;
+  int s0, s1;
+  int p = next_range(t, g, 0, s0, s1);
+  int st0 = s0;
+  Ahead<D> ahead0, ahead1;
+  if (st0 < s1) {
+    ahead0.load(str0, st0, s1);
+    ahead1.load(str1, st0, s1);
+  }
+  while (st0 < s1) {
+    const int end = min(st0 + kT, s1);               // of this tile's rows
+    __syncthreads();
+    ahead0.store(sStr0);
+    ahead1.store(sStr1);
+    if (!kDq) load_stats(st0, end, kT);
+    __syncthreads();
+    const int n = end - st0;
+    st0 += kT;
+    if (st0 >= s1) {
+      p = next_range(t, g, p, s0, s1);
+      st0 = s0;
+    }
+    if (st0 < s1) {
+      ahead0.load(str0, st0, s1);
+      ahead1.load(str1, st0, s1);
+    }
+    // rows of s are queries, columns keys
+    float s[RA][RB], dp[RA][RB];
+    dot_tile<D, RA, RB>(s, kDq ? sOwn0 : sStr0, kDq ? sStr0 : sOwn0, ty, tx);
+    dot_tile<D, RA, RB>(dp, kDq ? sOwn1 : sStr1, kDq ? sStr1 : sOwn1, ty, tx);
+    const int q1 = kDq ? own1 - own0 : n, k1 = kDq ? n : own1 - own0;
+#pragma unroll
+    for (int i = 0; i < RA; ++i)
+#pragma unroll
+      for (int j = 0; j < RB; ++j) {
+        const int r = RA * ty + i, c = tx + 16 * j;
+        const bool in = r < q1 && c < k1;
+        const float pij = in ? expf(fmaf(s[i][j], prm.scale, -sLse[r])) : 0.0f;
+        const float ds = in ? pij * (dp[i][j] - sDelta[r]) : 0.0f;
+        if (kDq) {
+          sP[c * S::kPRow + r] = ds;
+        } else {
+          sP[r * S::kPRow + c] = pij;
+          sdS[r * S::kPRow + c] = ds;
         }
-      __syncthreads();
-      if (kDq) {
-        add_product<D>(acc0, sP, sK, ty, tx);
-      } else {
-        add_product<D>(acc0, sdS, sQ, ty, tx);
-        add_product<D>(acc1, sP, sdO, ty, tx);
       }
-    }
+    __syncthreads();
+    add_product<D, RO>(acc0, kDq ? sP : sdS, sStr0, ty, tx);
+    if (!kDq) add_product<D, RO>(acc1, sP, sStr1, ty, tx);
   }
-  float* out0 = static_cast<float*>(kDq ? prm.dq : prm.dk) + head * D;
-  float* out1 = static_cast<float*>(prm.dv) + head * D;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int r = own0 + 4 * ty + i;
-    if (r >= own1) continue;
-#pragma unroll
-    for (int c = 0; c < D / 64; ++c) {
-      const size_t at = static_cast<size_t>(r) * D + 4 * tx + 64 * c;
-      store4(out0 + at, make_float4(acc0[i][4 * c] * prm.scale, acc0[i][4 * c + 1] * prm.scale,
-                                    acc0[i][4 * c + 2] * prm.scale, acc0[i][4 * c + 3] * prm.scale));
-      if (!kDq)
-        store4(out1 + at, make_float4(acc1[i][4 * c], acc1[i][4 * c + 1], acc1[i][4 * c + 2], acc1[i][4 * c + 3]));
-    }
-  }
+  store_tile<D, RO>(static_cast<float*>(kDq ? prm.dq : prm.dk) + head * D, acc0, prm.scale, own0, own1, ty, tx);
+  if (!kDq) store_tile<D, RO>(static_cast<float*>(prm.dv) + head * D, acc1, 1.0f, own0, own1, ty, tx);
 }
 
-template <int D>
+// One launch for both: the heavier blocks (dK, dV: four products) first.
+template <int D, int kOwn>
+__global__ void __launch_bounds__(kThreads, D == 64 ? 2 : 1) attn_bwd_fma_kernel(const __grid_constant__ BwdParams prm) {
+  extern __shared__ __align__(16) float smem[];
+  if (static_cast<int>(blockIdx.x) < prm.tiles_k)
+    fma_unit<D, kOwn, false>(prm, blockIdx.x, smem);
+  else
+    fma_unit<D, kOwn, true>(prm, blockIdx.x - prm.tiles_k, smem);
+}
+
+template <int D, int kOwn>
 int fma_impl(const BwdParams& prm, cudaStream_t st) {
-  constexpr int smem = Smem<D>::kBytes;
-  cudaError_t e = cudaFuncSetAttribute(attn_bwd_fma_kernel<D, false>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-  if (e == cudaSuccess)
-    e = cudaFuncSetAttribute(attn_bwd_fma_kernel<D, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  constexpr int smem = Smem<D, kOwn>::kBytes;
+  cudaError_t e = cudaFuncSetAttribute(attn_bwd_fma_kernel<D, kOwn>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return static_cast<int>(e);
-  attn_bwd_fma_kernel<D, false><<<dim3(prm.tiles_k, prm.BH), kThreads, smem, st>>>(prm);
-  attn_bwd_fma_kernel<D, true><<<dim3(prm.tiles_q, prm.BH), kThreads, smem, st>>>(prm);
+  attn_bwd_fma_kernel<D, kOwn><<<dim3(prm.tiles_k + prm.tiles_q, prm.BH), kThreads, smem, st>>>(prm);
   return static_cast<int>(cudaGetLastError());
 }
 
@@ -232,8 +296,6 @@ int delta_impl(const void* o, const void* dout, const float* dlse, float* delta,
 
 }  // namespace
 
-int attn_bwd_fma_tile_rows() { return kT; }
-
 int launch_delta(const void* o, const void* dout, const float* dlse, float* delta, long long rows, int D, int dtype,
                  cudaStream_t st) {
   if (dtype == PA_BF16)
@@ -243,8 +305,9 @@ int launch_delta(const void* o, const void* dout, const float* dlse, float* delt
                  : delta_impl<float, 128>(o, dout, dlse, delta, rows, st);
 }
 
-int launch_attn_bwd_fma(const BwdParams& prm, cudaStream_t st) {
-  return prm.D == 64 ? fma_impl<64>(prm, st) : fma_impl<128>(prm, st);
+int launch_attn_bwd_fma(const BwdParams& prm, int own_rows, cudaStream_t st) {
+  if (own_rows == 64) return prm.D == 64 ? fma_impl<64, 64>(prm, st) : fma_impl<128, 64>(prm, st);
+  return prm.D == 64 ? fma_impl<64, 32>(prm, st) : fma_impl<128, 32>(prm, st);
 }
 
 }  // namespace pa

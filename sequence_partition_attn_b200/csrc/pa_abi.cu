@@ -774,11 +774,17 @@ static int pa_attn_backward_impl(pa_ctx* ctx, const pa_attn_bwd_desc* d, void* s
     prm.N = d->N;
     prm.D = d->D;
     prm.scale = d->scale;
-    prm.tiles_q = fill_owner_tiles(prm.tq, pa::attn_bwd_fma_tile_rows());
-    prm.tiles_k = fill_owner_tiles(prm.tk, pa::attn_bwd_fma_tile_rows());
+    int own = 64;
+    prm.tiles_q = fill_owner_tiles(prm.tq, own);
+    prm.tiles_k = fill_owner_tiles(prm.tk, own);
+    if (BH * (prm.tiles_q + prm.tiles_k) < 2 * ctx->sm_count) {
+      own = 32;
+      prm.tiles_q = fill_owner_tiles(prm.tq, own);
+      prm.tiles_k = fill_owner_tiles(prm.tk, own);
+    }
     e = pa::launch_delta(d->o, d->dout, d->dlse, d->delta, rows, d->D, d->dtype, st);
     if (e) return cuda_fail(ctx, e, "delta launch");
-    e = pa::launch_attn_bwd_fma(prm, st);
+    e = pa::launch_attn_bwd_fma(prm, own, st);
     return e ? cuda_fail(ctx, e, "attention backward launch") : PA_OK;
   }
   pa::BwdTcParams tc;
