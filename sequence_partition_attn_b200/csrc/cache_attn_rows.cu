@@ -1,5 +1,10 @@
-// cache_attn_rows.cu -- attention over the 8-bit K/V cache for few query rows per KV head (bf16
-// queries: single tokens, a few tokens, heads that share a KV head).  Definition: cache_attn.cu.
+// cache_attn_rows.cu -- attention over the 8-bit K/V cache for few query rows per KV head (single
+// tokens, a few tokens, heads that share a KV head), and for fp32 queries of any number.
+//
+// For each request b, KV head and the R = (H / Hk) * Nq query rows that share it:
+//   lse_i = ln sum_{j < lens[b]} exp(scale q_i . k_j),  o_i = sum_j exp(s_ij - lse_i) v_j,
+// k_j = code * scale of its 64-token block.  Consecutive query heads share a KV head, so the R rows
+// are contiguous in q and o.
 //
 // Bound by reading the codes once: 2 D bytes per (token, KV head).  Up to 8 query rows cost the
 // same as one, so a shared KV head is read once for all its query heads.
@@ -8,7 +13,7 @@
 // units (request, KV head, 16-row tile) in a row are cut into equal shares, one per resident
 // block of threads, so one launch is one full wave whatever the lengths.  A share may begin and
 // end inside a unit; each piece writes its state in fp32 to a slot of its own and the join adds a
-// unit's pieces in order.  (Equal numbers of splits per request instead: a batch with lengths
+// unit's pieces in order, so results do not depend on the order in which blocks run.  (Equal numbers of splits per request instead: a batch with lengths
 // from 0 to 4096 took 26 us for 55 MB, nearly half of it on the longest request's blocks.)
 //
 // Each warp takes 16 tokens of every block and runs two tiles ahead with TMA loads into a ring of
@@ -31,6 +36,8 @@
 //     largest scale; p <= 2^8) and rounded to f16: 2^-11 relative, or 2^-32 of the row's largest
 //     weight where that is more.  A block whose scale is below 2^-16 of vmax would lose small
 //     weights that way: it takes bf16 (2^-8, any magnitude) instead.
+// fp32 queries take two f16 terms for each element of q and each weight (three bf16 ones in small
+// blocks): 22 bits, for twice the products and the same conversions.
 // The conversions (about 0.9 instructions per code) are what bounds a block of threads; with
 // queries as the 16 rows and V in bf16 throughout they were 1.6, and the kernel was held by them:
 // 64 us for the 236 MB of one 115200-token cache, 49% of the issue slots, 46% of DRAM.
@@ -52,21 +59,27 @@ constexpr float kUnit = 128.0f;        // weights are held as this times p vs / 
 constexpr float kSmallScale = 1.0f / 65536.0f;
 
 constexpr int kWideRows = 1024;        // query rows in all up to which the join takes a block per row
-constexpr int kMaxRows = 16;           // queries per tile: NT columns of 8, NT = 1 or 2
-__host__ __device__ constexpr int row_columns(int R) { return R <= 8 ? 1 : 2; }
-__host__ __device__ constexpr int resident(int nt) { return nt == 1 ? 4 : 3; }    // blocks of threads per SM
+constexpr int kMaxRows = 16;           // queries per tile: NT columns of 8, NT = 1 or 2 (fp32: 1)
+template <typename T>
+__host__ __device__ constexpr int row_columns(int R) { return R <= 8 || sizeof(T) == 4 ? 1 : 2; }
+// Blocks of threads per SM, by registers.
+template <typename T>
+__host__ __device__ constexpr int resident(int nt) { return nt == 1 && sizeof(T) == 2 ? 4 : 3; }
+constexpr float kLow = 4096.0f;        // the second f16 term of q is held times this
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kRescaleLog2 = 8.0f;   // move the running max only when it grows by more
 
-__device__ __forceinline__ uint32_t to_bf16(uint32_t f16) {
-  const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&f16));
-  return pack_bf16x2(f.x, f.y);
-}
-
 __device__ __forceinline__ uint32_t f16x2(float a, float b) {
   const __half2 h = __floats2half2_rn(a, b);
   return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+__device__ __forceinline__ float2 f16_values(uint32_t f16) { return __half22float2(*reinterpret_cast<const __half2*>(&f16)); }
+
+__device__ __forceinline__ uint32_t to_bf16(uint32_t f16) {
+  const float2 f = f16_values(f16);
+  return pack_bf16x2(f.x, f.y);
 }
 
 __device__ __forceinline__ void mma_f16(float (&c)[4], const uint32_t (&a)[4], const uint32_t (&b)[2]) {
@@ -185,10 +198,12 @@ struct Shared {
 
 // Blocks [blk0, blk1) of unit `unit`.  `slot` < 0: the piece is the whole unit and its state is
 // the result; else it goes to that slot of the scratch.
-template <int D, int NT>
+template <typename T, int D, int NT>
 __device__ __forceinline__ bool attend_piece(const CacheAttnRowsParams& par, uint8_t* smem, Shared& sh, Slot& into, Slot& from,
                                              long long unit, int len, int blk0, int blk1, long long slot) {
   const CacheAttnParams& prm = par.c;
+  constexpr bool kF32 = sizeof(T) == 4;
+  constexpr int kTerms = kF32 ? 2 : 1;   // f16 terms of q and of the weights
   constexpr int kRows = 8 * NT;
   constexpr int kSteps = D / 16;         // k-steps of S^T; 16-channel blocks of O^T
   using R = Ring<D>;
@@ -233,28 +248,23 @@ __device__ __forceinline__ bool attend_piece(const CacheAttnRowsParams& par, uin
 
   // q in f16, laid out as the codes are: column g of column block c; fq = softmax scale * log2(e) /
   // the row's power of two, moved to the lanes that hold the row's scores (rows 2t, 2t + 1).
-  uint32_t qb[NT][kSteps][2];
+  uint32_t qb[kTerms][NT][kSteps][2];
   float fq[NT][2];
 #pragma unroll
   for (int c = 0; c < NT; ++c) {
     const int r = row0 + 8 * c + g;
     float x[D / 4];
     float mx = 0.0f;
+    const T* src = static_cast<const T*>(prm.q) + (static_cast<size_t>(bh) * prm.R + min(r, prm.R - 1)) * D + t * 16;
 #pragma unroll
-    for (int a = 0; a < D / 64; ++a)
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        uint4 u = make_uint4(0u, 0u, 0u, 0u);
-        if (r < prm.R)
-          u = __ldg(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(prm.q) +
-                                                   (static_cast<size_t>(bh) * prm.R + r) * D + a * 64 + t * 16) + i);
-        const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          x[a * 16 + i * 8 + 2 * e] = __uint_as_float(w[e] << 16);
-          x[a * 16 + i * 8 + 2 * e + 1] = __uint_as_float(w[e] & 0xFFFF0000u);
-        }
-      }
+    for (int i = 0; i < D / 4; i += 4) {
+      const float4 u = load4(src + i / 16 * 64 + i % 16);
+      const bool in = r < prm.R;
+      x[i] = in ? u.x : 0.0f;
+      x[i + 1] = in ? u.y : 0.0f;
+      x[i + 2] = in ? u.z : 0.0f;
+      x[i + 3] = in ? u.w : 0.0f;
+    }
 #pragma unroll
     for (int i = 0; i < D / 4; ++i) mx = fmaxf(mx, fabsf(x[i]));
     mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
@@ -268,7 +278,14 @@ __device__ __forceinline__ bool attend_piece(const CacheAttnRowsParams& par, uin
 #pragma unroll
     for (int s = 0; s < kSteps; ++s)
 #pragma unroll
-      for (int i = 0; i < 2; ++i) qb[c][s][i] = f16x2(x[4 * s + 2 * i] * down, x[4 * s + 2 * i + 1] * down);
+      for (int i = 0; i < 2; ++i) {
+        const float a = x[4 * s + 2 * i] * down, b = x[4 * s + 2 * i + 1] * down;
+        qb[0][c][s][i] = f16x2(a, b);
+        if (kF32) {
+          const float2 h = f16_values(qb[0][c][s][i]);
+          qb[kTerms - 1][c][s][i] = f16x2((a - h.x) * kLow, (b - h.y) * kLow);
+        }
+      }
   }
 #pragma unroll
   for (int off = 16; off > 0; off >>= 1) vmax = fmaxf(vmax, __shfl_xor_sync(0xffffffffu, vmax, off));
@@ -305,7 +322,7 @@ __device__ __forceinline__ bool attend_piece(const CacheAttnRowsParams& par, uin
     from.next();
     if (tok >= end) continue;              // a warp without tokens in the last block
 
-    float s[NT][4] = {}, s2[NT][4] = {};       // two chains of products
+    float s[NT][4] = {}, s2[NT][4] = {};       // two chains of products; fp32: of q's two terms
 #pragma unroll
     for (int a = 0; a < D / 64; ++a) {
       const uint4 u0 = *reinterpret_cast<const uint4*>(tile + R::offset(xg, a * 64 + t * 16));
@@ -317,13 +334,16 @@ __device__ __forceinline__ bool attend_piece(const CacheAttnRowsParams& par, uin
         e4m3_to_f16(w0[e], k[0], k[2]);
         e4m3_to_f16(w1[e], k[1], k[3]);
 #pragma unroll
-        for (int c = 0; c < NT; ++c) mma_f16(e & 1 ? s2[c] : s[c], k, qb[c][4 * a + e]);
+        for (int c = 0; c < NT; ++c) {
+          mma_f16(!kF32 && (e & 1) ? s2[c] : s[c], k, qb[0][c][4 * a + e]);
+          if (kF32) mma_f16(s2[c], k, qb[kTerms - 1][c][4 * a + e]);
+        }
       }
     }
 #pragma unroll
     for (int c = 0; c < NT; ++c)
 #pragma unroll
-      for (int e = 0; e < 4; ++e) s[c][e] += s2[c][e];
+      for (int e = 0; e < 4; ++e) s[c][e] = kF32 ? fmaf(s2[c][e], 1.0f / kLow, s[c][e]) : s[c][e] + s2[c][e];
     const bool partial = tok + kTok > end;
     uint32_t v[4][D / 32];
 #pragma unroll
@@ -397,12 +417,19 @@ __device__ __forceinline__ bool attend_piece(const CacheAttnRowsParams& par, uin
       }
     const float unit = kUnit * ratio;
     if (ratio >= kSmallScale || !(ratio > 0.0f)) {
-      uint32_t pb[NT][2];
+      uint32_t pb[kTerms][NT][2];
 #pragma unroll
-      for (int c = 0; c < NT; ++c) {
-        pb[c][0] = transpose8(f16x2(p[c][0] * unit, p[c][1] * unit));
-        pb[c][1] = transpose8(f16x2(p[c][2] * unit, p[c][3] * unit));
-      }
+      for (int c = 0; c < NT; ++c)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const float a = p[c][2 * h] * unit, b = p[c][2 * h + 1] * unit;
+          const uint32_t w = f16x2(a, b);
+          pb[0][c][h] = transpose8(w);
+          if (kF32) {
+            const float2 v = f16_values(w);
+            pb[kTerms - 1][c][h] = transpose8(f16x2(a - v.x, b - v.y));
+          }
+        }
 #pragma unroll
       for (int w = 0; w < D / 32; ++w) {
         // bytes of two tokens side by side: channels 4 w + {0, 1} and + {2, 3}
@@ -414,18 +441,29 @@ __device__ __forceinline__ bool attend_piece(const CacheAttnRowsParams& par, uin
         e4m3_to_f16(lo23, b[0], b[1]);
         e4m3_to_f16(hi23, b[2], b[3]);
 #pragma unroll
-        for (int c = 0; c < NT; ++c) {
-          mma_f16(o[c][2 * w], a, pb[c]);
-          mma_f16(o[c][2 * w + 1], b, pb[c]);
-        }
+        for (int c = 0; c < NT; ++c)
+#pragma unroll
+          for (int e = 0; e < kTerms; ++e) {
+            mma_f16(o[c][2 * w], a, pb[e][c]);
+            mma_f16(o[c][2 * w + 1], b, pb[e][c]);
+          }
       }
     } else {
-      uint32_t pb[NT][2];
+      constexpr int kWide = kF32 ? 3 : 1;
+      uint32_t pb[kWide][NT][2];
 #pragma unroll
-      for (int c = 0; c < NT; ++c) {
-        pb[c][0] = transpose8(pack_bf16x2(p[c][0] * unit, p[c][1] * unit));
-        pb[c][1] = transpose8(pack_bf16x2(p[c][2] * unit, p[c][3] * unit));
-      }
+      for (int c = 0; c < NT; ++c)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          float a = p[c][2 * h] * unit, b = p[c][2 * h + 1] * unit;
+#pragma unroll
+          for (int e = 0; e < kWide; ++e) {
+            const uint32_t w = pack_bf16x2(a, b);
+            pb[e][c][h] = transpose8(w);
+            a -= __uint_as_float(w << 16);
+            b -= __uint_as_float(w & 0xFFFF0000u);
+          }
+        }
 #pragma unroll
       for (int w = 0; w < D / 32; ++w) {
         const uint32_t lo01 = __byte_perm(v[0][w], v[1][w], 0x5140), lo23 = __byte_perm(v[0][w], v[1][w], 0x7362);
@@ -441,10 +479,12 @@ __device__ __forceinline__ bool attend_piece(const CacheAttnRowsParams& par, uin
           b[i] = to_bf16(b[i]);
         }
 #pragma unroll
-        for (int c = 0; c < NT; ++c) {
-          mma_bf16(o[c][2 * w], a, pb[c]);
-          mma_bf16(o[c][2 * w + 1], b, pb[c]);
-        }
+        for (int c = 0; c < NT; ++c)
+#pragma unroll
+          for (int e = 0; e < kWide; ++e) {
+            mma_bf16(o[c][2 * w], a, pb[e][c]);
+            mma_bf16(o[c][2 * w + 1], b, pb[e][c]);
+          }
       }
     }
   }
@@ -500,7 +540,7 @@ __device__ __forceinline__ bool attend_piece(const CacheAttnRowsParams& par, uin
       if (c == 0) prm.ws_lse[at] = lse;
     } else {
       const size_t at = static_cast<size_t>(bh) * prm.R + row0 + r;
-      store4(static_cast<__nv_bfloat16*>(prm.o) + at * D + c, acc);
+      store4(static_cast<T*>(prm.o) + at * D + c, acc);
       if (c == 0) prm.lse[at] = lse;
     }
   }
@@ -509,8 +549,8 @@ __device__ __forceinline__ bool attend_piece(const CacheAttnRowsParams& par, uin
   return true;
 }
 
-template <int D, int NT>
-__global__ void __launch_bounds__(kWarps * 32, resident(NT)) cache_attn_rows_kernel(const __grid_constant__ CacheAttnRowsParams par) {
+template <typename T, int D, int NT>
+__global__ void __launch_bounds__(kWarps * 32, resident<T>(NT)) cache_attn_rows_kernel(const __grid_constant__ CacheAttnRowsParams par) {
   extern __shared__ uint8_t smem_raw[];
   __shared__ Shared sh;
   const CacheAttnParams& prm = par.c;
@@ -542,9 +582,9 @@ __global__ void __launch_bounds__(kWarps * 32, resident(NT)) cache_attn_rows_ker
     const int blk0 = max(p0 - kPieceCost, 0), blk1 = p1 - kPieceCost;
     if (blk1 > blk0) {
       const long long unit = static_cast<long long>(b) * prm.Hk * prm.row_tiles + in;
-      // shares and units both grow along the row of pieces, so their sum names a piece
-      const long long slot = blk0 == 0 && blk1 == nb ? -1 : blockIdx.x + unit;
-      if (!attend_piece<D, NT>(par, smem, sh, into, from, unit, cache_len(prm, b), blk0, blk1, slot)) return;
+      // a share has at most one piece that goes on with a unit, and one that a later share goes on with
+      const long long slot = blk0 == 0 && blk1 == nb ? -1 : 2LL * blockIdx.x + (blk0 == 0);
+      if (!attend_piece<T, D, NT>(par, smem, sh, into, from, unit, cache_len(prm, b), blk0, blk1, slot)) return;
     }
     x += p1 - p0;
   }
@@ -557,7 +597,7 @@ __global__ void __launch_bounds__(kWarps * 32, resident(NT)) cache_attn_rows_ker
 // done; rows without a token get the empty state.
 constexpr int kJoinWarps = 8;
 
-template <int D, bool kWide>
+template <typename T, int D, bool kWide>
 __global__ void __launch_bounds__(kJoinWarps * 32) cache_attn_rows_join_kernel(const __grid_constant__ CacheAttnParams prm) {
   constexpr int kC = D / 32;
   __shared__ float s_sum[kJoinWarps], s_acc[kJoinWarps][D];
@@ -569,7 +609,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) cache_attn_rows_join_kernel(c
   const int b = static_cast<int>(bh / prm.Hk);
   const Share share = work_share(prm, lane);
   const int nb = request_blocks(prm, b);
-  const int tile_rows = 8 * row_columns(prm.R);
+  const int tile_rows = 8 * row_columns<T>(prm.R);
   const long long unit = bh * prm.row_tiles + r / tile_rows;
   const long long first = places_before(prm, b, lane) * prm.Hk * prm.row_tiles +
                           (unit - static_cast<long long>(b) * prm.Hk * prm.row_tiles) * unit_places(nb) + kPieceCost;
@@ -577,9 +617,8 @@ __global__ void __launch_bounds__(kJoinWarps * 32) cache_attn_rows_join_kernel(c
   const long long p0 = first / share.size, p1 = (first + nb - 1) / share.size;
   if (nb > 0 && p0 == p1) return;
   const int pieces = nb > 0 ? static_cast<int>(p1 - p0 + 1) : 0;
-  const size_t slot0 = (p0 + unit) * prm.slot_rows + r % tile_rows;
-  const float* lse = prm.ws_lse + slot0;
-  const float* src = prm.ws_o + slot0 * D + lane * kC;
+  // piece i's row in the scratch: the first piece starts the unit, the others go on with it
+  auto at = [&](int i) { return static_cast<size_t>(2 * (p0 + i) + (i == 0)) * prm.slot_rows + r % tile_rows; };
   asm volatile("griddepcontrol.wait;" ::: "memory");           // the pieces are written
 
   constexpr int kStep = kWide ? kJoinWarps : 1;
@@ -588,19 +627,19 @@ __global__ void __launch_bounds__(kJoinWarps * 32) cache_attn_rows_join_kernel(c
   float acc[kC];
 #pragma unroll
   for (int c = 0; c < kC; ++c) acc[c] = 0.0f;
-  for (int i = lane; i < pieces; i += 32) m = fmaxf(m, lse[static_cast<size_t>(i) * prm.slot_rows]);
+  for (int i = lane; i < pieces; i += 32) m = fmaxf(m, prm.ws_lse[at(i)]);
 #pragma unroll
   for (int off = 16; off > 0; off >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
   for (int i0 = start; i0 < pieces; i0 += 32 * kStep) {
     const int n = min(32, (pieces - i0 + kStep - 1) / kStep);
-    const float own = lane < n ? expf(lse[static_cast<size_t>(i0 + lane * kStep) * prm.slot_rows] - m) : 0.0f;
+    const float own = lane < n ? expf(prm.ws_lse[at(i0 + lane * kStep)] - m) : 0.0f;
 #pragma unroll 8
     for (int i = 0; i < n; ++i) {
       const float w = __shfl_sync(0xffffffffu, own, i);
-      const float* at = src + static_cast<size_t>(i0 + i * kStep) * prm.slot_rows * D;
+      const float* src = prm.ws_o + at(i0 + i * kStep) * D + lane * kC;
       sum += w;
 #pragma unroll
-      for (int c = 0; c < kC; ++c) acc[c] = fmaf(w, at[c], acc[c]);
+      for (int c = 0; c < kC; ++c) acc[c] = fmaf(w, src[c], acc[c]);
     }
   }
   if (kWide) {
@@ -620,20 +659,25 @@ __global__ void __launch_bounds__(kJoinWarps * 32) cache_attn_rows_join_kernel(c
     }
   }
   const float inv = nb > 0 ? 1.0f / sum : 0.0f;
-  __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(prm.o) + row * D + lane * kC;
+  T* dst = static_cast<T*>(prm.o) + row * D + lane * kC;
 #pragma unroll
-  for (int c = 0; c < kC; c += 2) *reinterpret_cast<uint32_t*>(dst + c) = pack_bf16x2(acc[c] * inv, acc[c + 1] * inv);
+  for (int c = 0; c < kC; c += 2) {
+    if (sizeof(T) == 4)
+      *reinterpret_cast<float2*>(dst + c) = make_float2(acc[c] * inv, acc[c + 1] * inv);
+    else
+      *reinterpret_cast<uint32_t*>(dst + c) = pack_bf16x2(acc[c] * inv, acc[c + 1] * inv);
+  }
   if (lane == 0) prm.lse[row] = nb > 0 ? m + logf(sum) : -INFINITY;
 }
 
 // The join may be set up while the first kernel runs; it waits for all of it before it reads.
-template <int D, int NT>
+template <typename T, int D, int NT>
 int rows_impl(const CacheAttnRowsParams& par, cudaStream_t st) {
   constexpr int smem = Ring<D>::kBytes;
   const CacheAttnParams& prm = par.c;
-  cudaError_t e = cudaFuncSetAttribute(cache_attn_rows_kernel<D, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  cudaError_t e = cudaFuncSetAttribute(cache_attn_rows_kernel<T, D, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return static_cast<int>(e);
-  cache_attn_rows_kernel<D, NT><<<prm.shares, kWarps * 32, smem, st>>>(par);
+  cache_attn_rows_kernel<T, D, NT><<<prm.shares, kWarps * 32, smem, st>>>(par);
   if ((e = cudaGetLastError()) != cudaSuccess) return static_cast<int>(e);
   const bool wide = prm.rows <= kWideRows;
   cudaLaunchConfig_t cfg = {};
@@ -645,19 +689,26 @@ int rows_impl(const CacheAttnRowsParams& par, cudaStream_t st) {
   attr.val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
-  e = wide ? cudaLaunchKernelEx(&cfg, cache_attn_rows_join_kernel<D, true>, prm)
-           : cudaLaunchKernelEx(&cfg, cache_attn_rows_join_kernel<D, false>, prm);
+  e = wide ? cudaLaunchKernelEx(&cfg, cache_attn_rows_join_kernel<T, D, true>, prm)
+           : cudaLaunchKernelEx(&cfg, cache_attn_rows_join_kernel<T, D, false>, prm);
   return static_cast<int>(e);
 }
 
 }  // namespace
 
-int cache_attn_rows_tile_rows(int R) { return 8 * row_columns(R); }
-int cache_attn_rows_resident(int R) { return resident(row_columns(R)); }
+int cache_attn_rows_tile_rows(int R, int dtype) {
+  return 8 * (dtype == PA_F32 ? row_columns<float>(R) : row_columns<__nv_bfloat16>(R));
+}
+int cache_attn_rows_resident(int R, int dtype) {
+  return dtype == PA_F32 ? resident<float>(1) : resident<__nv_bfloat16>(row_columns<__nv_bfloat16>(R));
+}
 
-int launch_cache_attn_rows(const CacheAttnRowsParams& par, cudaStream_t st) {
-  if (row_columns(par.c.R) == 1) return par.c.D == 64 ? rows_impl<64, 1>(par, st) : rows_impl<128, 1>(par, st);
-  return par.c.D == 64 ? rows_impl<64, 2>(par, st) : rows_impl<128, 2>(par, st);
+int launch_cache_attn_rows(const CacheAttnRowsParams& par, int dtype, cudaStream_t st) {
+  const bool d64 = par.c.D == 64;
+  if (dtype == PA_F32) return d64 ? rows_impl<float, 64, 1>(par, st) : rows_impl<float, 128, 1>(par, st);
+  if (row_columns<__nv_bfloat16>(par.c.R) == 1)
+    return d64 ? rows_impl<__nv_bfloat16, 64, 1>(par, st) : rows_impl<__nv_bfloat16, 128, 1>(par, st);
+  return d64 ? rows_impl<__nv_bfloat16, 64, 2>(par, st) : rows_impl<__nv_bfloat16, 128, 2>(par, st);
 }
 
 }  // namespace pa

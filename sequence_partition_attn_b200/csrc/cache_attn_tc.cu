@@ -1,5 +1,5 @@
 // cache_attn_tc.cu -- attention over the 8-bit K/V cache for many query rows per KV head (bf16
-// queries: prompts, a ring step's block) on sm_100a tensor cores.  Definition: cache_attn.cu.
+// queries: prompts, a ring step's block) on sm_100a tensor cores.  Definition: cache_attn_rows.cu.
 //
 // Bound by the tensor cores and the exponentials, as the bf16 partition attention (attn_tc.cu),
 // whose scheme of two 128-row query tiles per CTA it follows: S = Q K^T and O += P V on tcgen05,
@@ -392,11 +392,42 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attn_tc_kernel(const __grid
   }
 }
 
+// Join of the splits' states: D / 4 threads per row, four channels each.
+template <int D>
+__global__ void __launch_bounds__(128) cache_join_kernel(const __grid_constant__ CacheAttnParams prm) {
+  constexpr int TPR = D / 4;
+  const long long row = static_cast<long long>(blockIdx.x) * (128 / TPR) + threadIdx.x / TPR;
+  const int c = threadIdx.x % TPR;
+  if (row >= prm.rows) return;
+  float m = -INFINITY;
+  for (int s = 0; s < prm.splits; ++s) m = fmaxf(m, prm.ws_lse[s * static_cast<size_t>(prm.rows) + row]);
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  float sum = 0.0f;
+  for (int s = 0; s < prm.splits; ++s) {
+    const size_t at = s * static_cast<size_t>(prm.rows) + row;
+    const float lse = prm.ws_lse[at];
+    const float w = lse == -INFINITY ? 0.0f : expf(lse - m);      // a split without tokens
+    const float4 x = *reinterpret_cast<const float4*>(prm.ws_o + at * D + 4 * c);
+    sum += w;
+    acc.x = fmaf(w, x.x, acc.x);
+    acc.y = fmaf(w, x.y, acc.y);
+    acc.z = fmaf(w, x.z, acc.z);
+    acc.w = fmaf(w, x.w, acc.w);
+  }
+  const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+  acc = make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
+  store4(static_cast<__nv_bfloat16*>(prm.o) + static_cast<size_t>(row) * D + 4 * c, acc);
+  if (c == 0) prm.lse[row] = sum == 0.0f ? -INFINITY : m + logf(sum);
+}
+
 template <int D>
 int tc_impl(const CacheAttnTcParams& p, unsigned units, cudaStream_t st) {
   cudaError_t e = cudaFuncSetAttribute(cache_attn_tc_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, Layout<D>::kBytes);
   if (e != cudaSuccess) return static_cast<int>(e);
   cache_attn_tc_kernel<D><<<units, kThreads, Layout<D>::kBytes, st>>>(p);
+  if ((e = cudaGetLastError()) != cudaSuccess || p.c.splits == 1) return static_cast<int>(e);
+  constexpr int kPerBlock = 128 / (D / 4);
+  cache_join_kernel<D><<<static_cast<unsigned>((p.c.rows + kPerBlock - 1) / kPerBlock), 128, 0, st>>>(p.c);
   return static_cast<int>(cudaGetLastError());
 }
 

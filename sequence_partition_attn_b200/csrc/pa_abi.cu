@@ -880,19 +880,18 @@ static int plan_cache_attn(pa_ctx* ctx, pa_dtype dtype, int B, int H, int Hk, in
   *ws_bytes = 0;
   if (R == 0) return PA_OK;
   prm.splits = 1;
-  if (dtype == PA_BF16 && !cache_attn_many_rows(dtype, R)) {
-    const int tile = pa::cache_attn_rows_tile_rows(prm.R);
+  if (!cache_attn_many_rows(dtype, R)) {
+    const int tile = pa::cache_attn_rows_tile_rows(prm.R, dtype);
     prm.row_tiles = (prm.R - 1) / tile + 1;
     prm.slot_rows = std::min(prm.R, tile);
-    prm.shares = ctx->sm_count * pa::cache_attn_rows_resident(prm.R);
-    *ws_bytes = static_cast<size_t>(prm.shares + BHk * prm.row_tiles) * prm.slot_rows * (D + 1) * sizeof(float);
+    prm.shares = ctx->sm_count * pa::cache_attn_rows_resident(prm.R, dtype);
+    *ws_bytes = 2 * static_cast<size_t>(prm.shares) * prm.slot_rows * (D + 1) * sizeof(float);
     return PA_OK;
   }
-  const int tile_rows = dtype == PA_BF16 ? pa::cache_attn_tc_block_rows() : pa::cache_attn_f32_tile_rows();
+  const int tile_rows = pa::cache_attn_tc_block_rows();
   const long long tiles = BHk * ((R - 1) / tile_rows + 1);
   // enough blocks to fill the GPU, each with a few cache blocks of tokens
-  const long long want = (dtype == PA_BF16 ? 1 : 4) * ctx->sm_count / tiles;
-  prm.splits = static_cast<int>(std::max(1LL, std::min(want, static_cast<long long>(prm.blocks) / 4)));
+  prm.splits = static_cast<int>(std::max(1LL, std::min(ctx->sm_count / tiles, static_cast<long long>(prm.blocks) / 4)));
   if (prm.splits > 1) *ws_bytes = static_cast<size_t>(prm.splits) * prm.rows * (D + 1) * sizeof(float);
   return PA_OK;
 }
@@ -942,19 +941,14 @@ static int pa_cache_attn_impl(pa_ctx* ctx, const pa_cache_attn_desc* d, void* st
     const long long units = static_cast<long long>(d->B) * d->Hk * tc.row_blocks * prm.splits;
     if (units > 0x7fffffffLL) return fail(ctx, PA_EINVAL, "too many work units");
     e = pa::launch_cache_attn_tc(tc, static_cast<unsigned>(units), st);
-  } else if (d->dtype == PA_BF16) {
+  } else {
     pa::CacheAttnRowsParams rows;
-    memset(&rows, 0, sizeof rows);
     rows.c = prm;
     if ((rc = encode_codes_map(ctx, &rows.tm_k, d->k_codes, d->B * d->Hk, d->M, d->D, pa::kCacheRowsBox))) return rc;
     if ((rc = encode_codes_map(ctx, &rows.tm_v, d->v_codes, d->B * d->Hk, d->M, d->D, pa::kCacheRowsBox))) return rc;
-    e = pa::launch_cache_attn_rows(rows, st);
-  } else {
-    e = pa::launch_cache_attn_f32(prm, st);
+    e = pa::launch_cache_attn_rows(rows, d->dtype, st);
   }
-  if (e) return cuda_fail(ctx, e, "cache attention launch");
-  if (prm.splits > 1) e = pa::launch_cache_join(prm, d->dtype, st);
-  return e ? cuda_fail(ctx, e, "cache join launch") : PA_OK;
+  return e ? cuda_fail(ctx, e, "cache attention launch") : PA_OK;
 }
 
 // With PA_DEBUG set when the context was created, every call synchronises its stream after

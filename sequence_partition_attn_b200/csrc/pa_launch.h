@@ -43,14 +43,11 @@ int launch_attn_bwd_tc(const BwdTcParams& prm, int D, cudaStream_t st);
 
 int launch_cache_store(const CacheStoreParams& prm, unsigned blocks, int dtype, int D, cudaStream_t st);
 
-int cache_attn_f32_tile_rows();
-int launch_cache_attn_f32(const CacheAttnParams& prm, cudaStream_t st);
-int cache_attn_rows_tile_rows(int R);
-int cache_attn_rows_resident(int R);        // blocks of threads per SM, each with a share of the work
+int cache_attn_rows_tile_rows(int R, int dtype);
+int cache_attn_rows_resident(int R, int dtype);     // blocks of threads per SM, each with a share of the work
 constexpr int kCacheRowsBox = 16;       // tokens per box of its tensor maps
-int launch_cache_attn_rows(const CacheAttnRowsParams& par, cudaStream_t st);
+int launch_cache_attn_rows(const CacheAttnRowsParams& par, int dtype, cudaStream_t st);
 int cache_attn_tc_block_rows();
 int launch_cache_attn_tc(const CacheAttnTcParams& p, unsigned units, cudaStream_t st);
-int launch_cache_join(const CacheAttnParams& prm, int dtype, cudaStream_t st);
 
 }  // namespace pa
