@@ -10,6 +10,7 @@
 // Storing rows behind a block's earlier tokens keeps the larger of the two scales.  If the
 // scale grows, the older codes are rounded once more to the new one, which is exact unless they
 // fall below e4m3's normal range.
+#include <cuda_fp16.h>
 #include <cuda_fp8.h>
 
 #include "pa_device.cuh"
@@ -20,31 +21,37 @@ namespace {
 
 constexpr int kTok = PA_CACHE_BLOCK;
 constexpr int kThreads = 256;
-constexpr int kSeg = 16;              // channels per item: one 16-byte code store
+constexpr int kSeg = 8;               // channels per item: 16 (or 32) bytes in, 8 out
 
+// An item's values as loaded; they are widened twice, for the maximum and for the codes, rather
+// than held in fp32: twice the blocks fit an SM.
 template <typename T>
-__device__ __forceinline__ void load16(const T* p, float (&x)[kSeg]);
-template <>
-__device__ __forceinline__ void load16<float>(const float* p, float (&x)[kSeg]) {
+struct Raw {
+  static constexpr int kN = kSeg * sizeof(T) / 16;
+  uint4 v[kN];
+  __device__ __forceinline__ void load(const T* p) {
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const float4 v = __ldg(reinterpret_cast<const float4*>(p) + i);
-    x[4 * i] = v.x; x[4 * i + 1] = v.y; x[4 * i + 2] = v.z; x[4 * i + 3] = v.w;
+    for (int i = 0; i < kN; ++i) v[i] = __ldg(reinterpret_cast<const uint4*>(p) + i);
   }
-}
-template <>
-__device__ __forceinline__ void load16<__nv_bfloat16>(const __nv_bfloat16* p, float (&x)[kSeg]) {
+  __device__ __forceinline__ void values(float (&x)[kSeg]) const {
+    const uint32_t w[4 * kN] = {v[0].x, v[0].y, v[0].z, v[0].w};
+    if (sizeof(T) == 4) {
 #pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const uint4 v = __ldg(reinterpret_cast<const uint4*>(p) + i);
-    const uint32_t u[4] = {v.x, v.y, v.z, v.w};
+      for (int i = 0; i < kN; ++i) {
+        x[4 * i] = __uint_as_float(v[i].x);
+        x[4 * i + 1] = __uint_as_float(v[i].y);
+        x[4 * i + 2] = __uint_as_float(v[i].z);
+        x[4 * i + 3] = __uint_as_float(v[i].w);
+      }
+    } else {
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      x[8 * i + 2 * j] = __uint_as_float(u[j] << 16);
-      x[8 * i + 2 * j + 1] = __uint_as_float(u[j] & 0xFFFF0000u);
+      for (int i = 0; i < 4; ++i) {
+        x[2 * i] = __uint_as_float(w[i] << 16);
+        x[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+      }
     }
   }
-}
+};
 
 // Smallest 2^e >= amax / 448 with e >= -126 (amax > 0, finite): 448 = 1.75 * 2^8.
 __device__ __forceinline__ float block_scale(float amax) {
@@ -54,34 +61,38 @@ __device__ __forceinline__ float block_scale(float amax) {
   return __uint_as_float(static_cast<uint32_t>(e + 127) << 23);
 }
 
-__device__ __forceinline__ uint4 encode16(const float (&x)[kSeg], float inv) {
-  uint32_t w[4];
+__device__ __forceinline__ uint2 encode(const float (&x)[kSeg], float inv) {
+  uint32_t w[2];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
+  for (int i = 0; i < 2; ++i) {
     const __nv_fp8x2_storage_t lo = __nv_cvt_float2_to_fp8x2(make_float2(x[4 * i] * inv, x[4 * i + 1] * inv), __NV_SATFINITE, __NV_E4M3);
     const __nv_fp8x2_storage_t hi = __nv_cvt_float2_to_fp8x2(make_float2(x[4 * i + 2] * inv, x[4 * i + 3] * inv), __NV_SATFINITE, __NV_E4M3);
     w[i] = static_cast<uint32_t>(lo) | (static_cast<uint32_t>(hi) << 16);
   }
-  return make_uint4(w[0], w[1], w[2], w[3]);
+  return make_uint2(w[0], w[1]);
 }
 
-__device__ __forceinline__ void decode16(uint4 c, float (&x)[kSeg]) {
-  const uint32_t w[4] = {c.x, c.y, c.z, c.w};
+__device__ __forceinline__ void decode(uint2 c, float (&x)[kSeg]) {
+  const uint32_t w[2] = {c.x, c.y};
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(w[i >> 1] >> (16 * (i & 1))), __NV_E4M3);
-    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h));
-    x[2 * i] = f.x;
-    x[2 * i + 1] = f.y;
+  for (int i = 0; i < 2; ++i) {
+    uint32_t h[2];
+    e4m3_to_f16(w[i], h[0], h[1]);
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h[j]));
+      x[4 * i + 2 * j] = f.x;
+      x[4 * i + 2 * j + 1] = f.y;
+    }
   }
 }
 
 // One block of threads per cache block that the new rows touch, for K or V of one head.  Bound
 // by HBM: the rows are read once into registers, reduced, and written as codes.
 template <typename T, int D>
-__global__ void __launch_bounds__(kThreads) cache_store_kernel(const __grid_constant__ CacheStoreParams prm) {
+__global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 8 : 5) cache_store_kernel(const __grid_constant__ CacheStoreParams prm) {
   constexpr int kSegs = D / kSeg;
-  constexpr int kItems = kTok * kSegs / kThreads;      // (token, 16 channels) items per thread
+  constexpr int kItems = kTok * kSegs / kThreads;      // (token, 8 channels) items per thread
   __shared__ float s_max[kThreads / 32];
   const int i = blockIdx.x % prm.touched;
   const int kv = (blockIdx.x / prm.touched) & 1;
@@ -100,17 +111,23 @@ __global__ void __launch_bounds__(kThreads) cache_store_kernel(const __grid_cons
   float* scale = (kv ? prm.v_scale : prm.k_scale) + static_cast<size_t>(bh) * prm.blocks + blk;
   const float had = tok0 < t0 ? *scale : 0.0f;
 
-  float x[kItems][kSeg];
+  Raw<T> raw[kItems];
   float amax = 0.0f;
 #pragma unroll
   for (int n = 0; n < kItems; ++n) {
     const int idx = n * kThreads + threadIdx.x;
     const int row = tok0 + idx / kSegs - t0;
+    if (row >= 0 && row < prm.T) raw[n].load(src + static_cast<size_t>(row) * D + (idx % kSegs) * kSeg);
+  }
+#pragma unroll
+  for (int n = 0; n < kItems; ++n) {
+    const int row = tok0 + (n * kThreads + threadIdx.x) / kSegs - t0;
     if (row < 0 || row >= prm.T) continue;
-    load16<T>(src + static_cast<size_t>(row) * D + (idx % kSegs) * kSeg, x[n]);
+    float x[kSeg];
+    raw[n].values(x);
 #pragma unroll
     for (int c = 0; c < kSeg; ++c) {
-      const float a = fabsf(x[n][c]);
+      const float a = fabsf(x[c]);
       if (a < INFINITY) amax = fmaxf(amax, a);         // infinities saturate, NaN stays NaN: neither sets the scale
     }
   }
@@ -130,13 +147,14 @@ __global__ void __launch_bounds__(kThreads) cache_store_kernel(const __grid_cons
     const int idx = n * kThreads + threadIdx.x;
     const int tok = idx / kSegs;
     const int row = tok0 + tok - t0;
-    uint4* dst = reinterpret_cast<uint4*>(codes + static_cast<size_t>(tok) * D + (idx % kSegs) * kSeg);
+    uint2* dst = reinterpret_cast<uint2*>(codes + static_cast<size_t>(tok) * D + (idx % kSegs) * kSeg);
+    float x[kSeg];
     if (row >= 0 && row < prm.T) {
-      *dst = encode16(x[n], inv);
+      raw[n].values(x);
+      *dst = encode(x, inv);
     } else if (row < 0 && now > had) {
-      float old[kSeg];
-      decode16(*dst, old);
-      *dst = encode16(old, had * inv);
+      decode(*dst, x);
+      *dst = encode(x, had * inv);
     }
   }
   if (threadIdx.x == 0) *scale = now;
