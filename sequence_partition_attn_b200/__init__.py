@@ -320,6 +320,33 @@ def _maybe(ctx, name, t, shape, dtype):
     return 0 if t is None else _want(ctx, name, t, shape, dtype)
 
 
+_TORCH = None
+
+
+def _torch():
+    global _TORCH
+    if _TORCH is None:
+        import torch
+        _TORCH = torch
+    return _TORCH
+
+
+def _code(t):
+    """pa_dtype of a tensor."""
+    code = _CODES.get(t.dtype)
+    if code is None:
+        code = _CODES[t.dtype] = _dtype_code(t)
+    return code
+
+
+_CODES = {}
+
+
+def _call(ctx, rc):
+    if rc != 0:
+        _check(ctx._ptr, rc)
+
+
 def _four(name, t):
     if t.dim() != 4:
         raise PAError(-1, f"{name} has shape {tuple(t.shape)}, expected four dimensions")
@@ -335,9 +362,8 @@ def _address(a):
 
 
 def _raw_stream(ctx, stream):
-    import torch
     if stream is None:
-        return torch._C._cuda_getCurrentRawStream(ctx.device)
+        return _torch()._C._cuda_getCurrentRawStream(ctx.device)
     return stream if isinstance(stream, int) else stream.cuda_stream
 
 
@@ -348,10 +374,10 @@ def pa_attn_backward(ctx: Context, q, k, v, o, lse, do, part_off, G, fresh, dq, 
     Reused states are constants; a row without a fresh pair gets zeros.  delta [B, H, N] f32
     receives do.o - dlse and is the call's only scratch.  part_off, G, fresh and scale as in
     the forward call."""
-    import torch
+    torch = _torch()
     full = B, H, N, D = _four("q", q)
     row, dt, f32 = (B, H, N), q.dtype, torch.float32
-    code = _dtype_code(q)
+    code = _code(q)
     off, fr, G = _host_i32(part_off), _host_u8(fresh), int(G)
     _want_mask(off, G, fr)
     d = _ATTN_BWD.pack(
@@ -360,7 +386,7 @@ def pa_attn_backward(ctx: Context, q, k, v, o, lse, do, part_off, G, fresh, dq, 
         _want(ctx, "do", do, full, dt), _maybe(ctx, "dlse", dlse, row, f32), off.size - 1, _address(off), G,
         _address(fr), _want(ctx, "dq", dq, full, dt), _want(ctx, "dk", dk, full, dt),
         _want(ctx, "dv", dv, full, dt), _want(ctx, "delta", delta, row, f32))
-    _check(ctx.ptr, lib().pa_attn_backward(ctx.ptr, d, _raw_stream(ctx, stream)))
+    _call(ctx, lib().pa_attn_backward(ctx._ptr, d, _raw_stream(ctx, stream)))
 
 
 def _want_mask(off, G, fr):
@@ -374,7 +400,7 @@ def _want_mask(off, G, fr):
 
 
 def _cache_args(ctx, kc, vc, k_scale, v_scale):
-    import torch
+    torch = _torch()
     full = B, Hk, M, D = _four("kc", kc)
     code = torch.uint8 if kc.dtype is torch.uint8 else torch.float8_e4m3fn
     blocks = (B, Hk, -(-M // PA_CACHE_BLOCK))
@@ -387,14 +413,14 @@ def pa_cache_store(ctx: Context, k, v, start, kc, vc, k_scale, v_scale, stream=N
     """Round k, v [B, Hk, T, D] (bf16 or f32) into the 8-bit cache kc, vc [B, Hk, M, D]
     (float8_e4m3fn, or uint8 holding the codes) with scales [B, Hk, ceil(M / 64)] f32, at token
     offsets start (int32 [B] on the device, or None for 0)."""
-    import torch
+    torch = _torch()
     B, Hk, M, D, pk, pv, pks, pvs = _cache_args(ctx, kc, vc, k_scale, v_scale)
     T = _four("k", k)[2]
     rows = (B, Hk, T, D)
-    d = _CACHE_STORE.pack(_dtype_code(k), B, Hk, T, M, D, _want(ctx, "k", k, rows, k.dtype),
+    d = _CACHE_STORE.pack(_code(k), B, Hk, T, M, D, _want(ctx, "k", k, rows, k.dtype),
                           _want(ctx, "v", v, rows, k.dtype), _maybe(ctx, "start", start, (B,), torch.int32),
                           pk, pv, pks, pvs)
-    _check(ctx.ptr, lib().pa_cache_store(ctx.ptr, d, _raw_stream(ctx, stream)))
+    _call(ctx, lib().pa_cache_store(ctx._ptr, d, _raw_stream(ctx, stream)))
 
 
 def cache_attn_workspace(ctx: Context, q, kc):
@@ -414,7 +440,7 @@ def pa_cache_attn(ctx: Context, q, kc, vc, k_scale, v_scale, lens, o, lse, scale
     tokens (int32 [B] on the device, or None for all M) of the 8-bit cache; H is a multiple of
     the cache's Hk.  workspace: from cache_attn_workspace; without one the call takes it from
     torch's allocator."""
-    import torch
+    torch = _torch()
     B, Hk, M, D, pk, pv, pks, pvs = _cache_args(ctx, kc, vc, k_scale, v_scale)
     _, H, Nq, _ = _four("q", q)
     rows, dt = (B, H, Nq, D), q.dtype
@@ -426,11 +452,11 @@ def pa_cache_attn(ctx: Context, q, kc, vc, k_scale, v_scale, lens, o, lse, scale
             # allocated for the current stream: not handed out again before `s` is done with it
             workspace.record_stream(torch.cuda.ExternalStream(s, device=workspace.device))
     size = workspace.numel()
-    d = _CACHE_ATTN.pack(_dtype_code(q), B, H, Hk, Nq, M, D, _scale(scale, D), pq, pk, pv, pks, pvs,
+    d = _CACHE_ATTN.pack(_code(q), B, H, Hk, Nq, M, D, _scale(scale, D), pq, pk, pv, pks, pvs,
                          _maybe(ctx, "lens", lens, (B,), torch.int32), _want(ctx, "o", o, rows, dt),
                          _want(ctx, "lse", lse, (B, H, Nq), torch.float32),
                          _want(ctx, "workspace", workspace, (size,), torch.uint8) if size else 0, size)
-    _check(ctx.ptr, lib().pa_cache_attn(ctx.ptr, d, s))
+    _call(ctx, lib().pa_cache_attn(ctx._ptr, d, s))
 
 
 def select_fresh(w_stored, G: int, threshold: float) -> np.ndarray:

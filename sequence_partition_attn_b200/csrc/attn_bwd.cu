@@ -26,6 +26,7 @@ __global__ void __launch_bounds__(256) delta_kernel(const T* __restrict__ o, con
                                                     const float* __restrict__ dlse, float* __restrict__ delta,
                                                     long long rows) {
   constexpr int kLanes = D * sizeof(T) / 16;
+  asm volatile("griddepcontrol.launch_dependents;");
   const long long row = (static_cast<long long>(blockIdx.x) * 256 + threadIdx.x) / kLanes;
   const int c = threadIdx.x % kLanes;
   float sum = 0.0f;

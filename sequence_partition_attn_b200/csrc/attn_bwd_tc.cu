@@ -49,7 +49,8 @@ __device__ __forceinline__ void read_scores(uint32_t tmem, float (&s)[64]) {
   for (int i = 0; i < 64; ++i) s[i] = __uint_as_float(r[i]);
 }
 
-__device__ __forceinline__ bool has_short_range(const AttnTables& t, int g) {
+template <int MP>
+__device__ __forceinline__ bool has_short_range(const BwdSide<MP>& t, int g) {
   for (int p = 0; p < t.P;) {
     int s0, s1;
     p = next_range(t, g, p, s0, s1);
@@ -59,15 +60,16 @@ __device__ __forceinline__ bool has_short_range(const AttnTables& t, int g) {
 }
 
 // The group, head and first row of a unit: groups in launch order, heads and then tiles in each.
-__device__ __forceinline__ int owner_tile(const BwdSide& side, int unit, int& bh, int& own0) {
+template <int MP>
+__device__ __forceinline__ int owner_tile(const BwdSide<MP>& side, int unit, int& bh, int& own0) {
   int i = 0;
   while (side.unit_start[i + 1] <= unit) ++i;
   const int g = side.order[i];
-  const int rows = side.t.qg_row0[g + 1] - side.t.qg_row0[g];
+  const int rows = side.qg_row0[g + 1] - side.qg_row0[g];
   const int tiles = (rows + kRows - 1) / kRows;
   const int local = unit - side.unit_start[i];
   bh = local / tiles;
-  own0 = side.t.qg_row0[g] + (local - bh * tiles) * kRows;
+  own0 = side.qg_row0[g] + (local - bh * tiles) * kRows;
   return g;
 }
 
@@ -101,13 +103,13 @@ struct KvLayout {
   static_assert(kBytes <= 227 * 1024, "shared memory budget");
 };
 
-template <int D>
-__device__ __forceinline__ void dkdv_unit(const BwdTcParams& prm, int unit, uint8_t* gbase, const uint32_t base) {
+template <int D, int MP>
+__device__ __forceinline__ void dkdv_unit(const BwdTcParams<MP>& prm, int unit, uint8_t* gbase, const uint32_t base) {
   using L = KvLayout<D>;
   auto bar = [&](int i) { return base + L::kBar + 8u * i; };
   volatile int* abort_flag = reinterpret_cast<volatile int*>(gbase + L::kAbort);
   int* status = prm.status;
-  const AttnTables& t = prm.kv.t;
+  const BwdSide<MP>& t = prm.kv;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   int bh, own0;
   const int g = owner_tile(prm.kv, unit, bh, own0);
@@ -232,6 +234,7 @@ __device__ __forceinline__ void dkdv_unit(const BwdTcParams& prm, int unit, uint
     } else if (warp == 3) {
       // ---------------------------------------------------------------- LSE and delta
       const size_t head = static_cast<size_t>(bh) * prm.N;
+      asm volatile("griddepcontrol.wait;" ::: "memory");       // delta is written
       int j = 0;
       for (TileWalk w(t, g); w.valid(); w.next(), ++j) {
         const int s = j & 1;
@@ -363,13 +366,13 @@ struct QLayout {
   static_assert(kBytes <= 227 * 1024, "shared memory budget");
 };
 
-template <int D>
-__device__ __forceinline__ void dq_unit(const BwdTcParams& prm, int unit, uint8_t* gbase, const uint32_t base) {
+template <int D, int MP>
+__device__ __forceinline__ void dq_unit(const BwdTcParams<MP>& prm, int unit, uint8_t* gbase, const uint32_t base) {
   using L = QLayout<D>;
   auto bar = [&](int i) { return base + L::kBar + 8u * i; };
   volatile int* abort_flag = reinterpret_cast<volatile int*>(gbase + L::kAbort);
   int* status = prm.status;
-  const AttnTables& t = prm.q.t;
+  const BwdSide<MP>& t = prm.q;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   int bh, own0;
   const int g = owner_tile(prm.q, unit, bh, own0);
@@ -428,7 +431,7 @@ __device__ __forceinline__ void dq_unit(const BwdTcParams& prm, int unit, uint8_
         TileWalk wk(t, g), wv(t, g);
         const bool shorts = has_short_range(t, g);
         // A tile arrived: zero behind a short range.
-        auto fix = [&](TileWalk& w, int at) {
+        auto fix = [&](auto& w, int at) {
           if (w.is_short()) zero_rows<D>(gbase + at, w.last());
           w.next();
         };
@@ -497,6 +500,7 @@ __device__ __forceinline__ void dq_unit(const BwdTcParams& prm, int unit, uint8_
     const uint32_t lane_off = (static_cast<uint32_t>((warp & 3) * 32) << 16) + x * 64;
     const bool row_ok = own0 + row < own1;
     const size_t at = static_cast<size_t>(bh) * prm.N + own0 + row;
+    asm volatile("griddepcontrol.wait;" ::: "memory");         // delta is written
     const float l = row_ok ? prm.lse[at] : -INFINITY;
     const float nl = l == -INFINITY ? -INFINITY : -l * kLog2e;    // no key: every P is 0
     const float nd = row_ok ? -prm.delta[at] : 0.0f;
@@ -563,8 +567,8 @@ __device__ __forceinline__ void dq_unit(const BwdTcParams& prm, int unit, uint8_
 
 // One launch: the CTAs of the dK, dV kernel first, those of dQ behind them, each longest first (the
 // hardware hands them out in order), so that there is one tail instead of two.
-template <int D>
-__global__ void __launch_bounds__(kThreads, 1) attn_bwd_tc_kernel(const __grid_constant__ BwdTcParams prm) {
+template <int D, int MP>
+__global__ void __launch_bounds__(kThreads, 1) attn_bwd_tc_kernel(const __grid_constant__ BwdTcParams<MP> prm) {
   extern __shared__ __align__(1024) uint8_t smem[];
   const uint32_t base = smem_u32(smem);
   if (!smem_aligned(base, prm.status)) return;
@@ -574,21 +578,35 @@ __global__ void __launch_bounds__(kThreads, 1) attn_bwd_tc_kernel(const __grid_c
     dq_unit<D>(prm, blockIdx.x - prm.kv.units, smem, base);
 }
 
-template <int D>
-int tc_impl(const BwdTcParams& prm, cudaStream_t st) {
+// Launched ahead of the end of the delta kernel, whose results alone are waited for.
+template <int D, int MP>
+int tc_impl(const BwdTcParams<MP>& prm, cudaStream_t st) {
   constexpr int smem = KvLayout<D>::kBytes > QLayout<D>::kBytes ? KvLayout<D>::kBytes : QLayout<D>::kBytes;
-  cudaError_t e = cudaFuncSetAttribute(attn_bwd_tc_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  cudaError_t e = cudaFuncSetAttribute(attn_bwd_tc_kernel<D, MP>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return static_cast<int>(e);
-  attn_bwd_tc_kernel<D><<<prm.kv.units + prm.q.units, kThreads, smem, st>>>(prm);
-  return static_cast<int>(cudaGetLastError());
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(prm.kv.units + prm.q.units);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr = {};
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return static_cast<int>(cudaLaunchKernelEx(&cfg, attn_bwd_tc_kernel<D, MP>, prm));
 }
 
 }  // namespace
 
 int attn_bwd_tc_tile_rows() { return kRows; }
 
-int launch_attn_bwd_tc(const BwdTcParams& prm, int D, cudaStream_t st) {
-  return D == 64 ? tc_impl<64>(prm, st) : tc_impl<128>(prm, st);
+int launch_attn_bwd_tc(const BwdTcParams<32>& prm, int D, cudaStream_t st) {
+  return D == 64 ? tc_impl<64, 32>(prm, st) : tc_impl<128, 32>(prm, st);
+}
+
+int launch_attn_bwd_tc(const BwdTcParams<PA_MAX_P>& prm, int D, cudaStream_t st) {
+  return D == 64 ? tc_impl<64, PA_MAX_P>(prm, st) : tc_impl<128, PA_MAX_P>(prm, st);
 }
 
 }  // namespace pa

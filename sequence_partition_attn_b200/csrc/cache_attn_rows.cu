@@ -53,7 +53,7 @@ constexpr int kWarps = 4;
 constexpr int kTok = 16;               // tokens per tile
 constexpr int kStages = 3;             // tiles in shared memory per warp
 constexpr int kPieceCost = 4;          // what a piece costs besides its blocks, in blocks
-constexpr int kMinPlaces = 8;          // places per share, at least
+constexpr int kMinPlaces = 6;          // places per share, at least
 static_assert(kWarps * kTok == PA_CACHE_BLOCK, "the warps share one cache block");
 constexpr float kUnit = 128.0f;        // weights are held as this times p vs / vmax
 constexpr float kSmallScale = 1.0f / 65536.0f;
@@ -137,44 +137,56 @@ __device__ __forceinline__ int request_blocks(const CacheAttnParams& prm, int b)
 }
 __device__ __forceinline__ int unit_places(int blocks) { return blocks > 0 ? blocks + kPieceCost : 0; }
 
-// Sum over requests [0, n) of their places, for one KV head and row tile.
-__device__ __forceinline__ long long places_before(const CacheAttnParams& prm, int n, int lane) {
-  long long sum = 0;
-  for (int b = lane; b < n; b += 32) sum += unit_places(request_blocks(prm, b));
-#pragma unroll
-  for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
-  return sum;
-}
-
-__device__ __forceinline__ Share work_share(const CacheAttnParams& prm, int lane) {
-  Share s;
-  s.total = places_before(prm, prm.B, lane) * prm.Hk * prm.row_tiles;
-  s.size = max((s.total + prm.shares - 1) / prm.shares, static_cast<long long>(kMinPlaces));
-  return s;
-}
-
-// Request that holds place x, and its first place.
-__device__ __forceinline__ int find_request(const CacheAttnParams& prm, long long x, int lane, long long& first) {
-  long long before = 0;
-  for (int b0 = 0; b0 < prm.B; b0 += 32) {
-    const int b = b0 + lane;
-    const long long own = b < prm.B ? static_cast<long long>(unit_places(request_blocks(prm, b))) * prm.Hk * prm.row_tiles : 0;
-    long long upto = own;
+// The lengths of 32 requests at a time, one per lane: up to 32 requests are read once.
+struct Requests {
+  const CacheAttnParams& prm;
+  int lane, base, nb;                    // request base + lane has nb blocks
+  long long upto, sum;                   // places (of one KV head and row tile) up to and with it; of all 32
+  __device__ __forceinline__ Requests(const CacheAttnParams& p, int l) : prm(p), lane(l) { read(0); }
+  __device__ __forceinline__ void read(int b0) {
+    base = b0;
+    nb = b0 + lane < prm.B ? request_blocks(prm, b0 + lane) : 0;
+    upto = unit_places(nb);
 #pragma unroll
     for (int off = 1; off < 32; off <<= 1) {
       const long long y = __shfl_up_sync(0xffffffffu, upto, off);
       if (lane >= off) upto += y;
     }
-    const uint32_t hit = __ballot_sync(0xffffffffu, before + upto > x);
-    if (hit) {
-      const int l = __ffs(hit) - 1;
-      first = before + __shfl_sync(0xffffffffu, upto - own, l);
-      return b0 + l;
-    }
-    before += __shfl_sync(0xffffffffu, upto, 31);
+    sum = __shfl_sync(0xffffffffu, upto, 31);
   }
-  first = before;
-  return prm.B;
+  __device__ __forceinline__ int blocks(int b) {
+    if ((b & ~31) != base) read(b & ~31);
+    return __shfl_sync(0xffffffffu, nb, b & 31);
+  }
+  __device__ __forceinline__ long long before(int b) {           // places of requests [0, b)
+    long long acc = 0;
+    for (int b0 = 0; b0 < b; b0 += 32) {
+      if (base != b0) read(b0);
+      acc += b0 + 32 <= b ? sum : __shfl_sync(0xffffffffu, upto, (b - 1) & 31);
+    }
+    return acc;
+  }
+  // Request that holds place x of all requests (x in units of one KV head and row tile), and its first.
+  __device__ __forceinline__ int find(long long x, long long& first) {
+    long long acc = 0;
+    for (int b0 = 0;; b0 += 32) {
+      if (base != b0) read(b0);
+      const uint32_t hit = __ballot_sync(0xffffffffu, acc + upto > x);
+      if (hit) {
+        const int l = __ffs(hit) - 1;
+        first = acc + __shfl_sync(0xffffffffu, upto - unit_places(nb), l);
+        return b0 + l;
+      }
+      acc += sum;
+    }
+  }
+};
+
+__device__ __forceinline__ Share work_share(const CacheAttnParams& prm, Requests& req) {
+  Share s;
+  s.total = req.before(prm.B) * prm.Hk * prm.row_tiles;
+  s.size = max((s.total + prm.shares - 1) / prm.shares, static_cast<long long>(kMinPlaces));
+  return s;
 }
 
 // ------------------------------------------------------------------ one piece of a unit
@@ -562,18 +574,21 @@ __global__ void __launch_bounds__(kWarps * 32, resident<T>(NT)) cache_attn_rows_
   __syncthreads();
   Slot into, from;                         // this warp's next tile to load, to use
   const int lane = threadIdx.x & 31;
-  const Share share = work_share(prm, lane);
+  Requests req(prm, lane);
+  const Share share = work_share(prm, req);
   long long x = blockIdx.x * share.size;
   const long long stop = min(x + share.size, share.total);
   if (x >= stop) return;
+  const long long units = static_cast<long long>(prm.Hk) * prm.row_tiles;         // of a request
   long long first;
-  int b = find_request(prm, x, lane, first);
-  int nb = request_blocks(prm, b);
+  int b = req.find(x / units, first);
+  first *= units;
+  int nb = req.blocks(b);
   while (x < stop) {
     const long long places = unit_places(nb);
-    if (x >= first + places * prm.Hk * prm.row_tiles) {          // on to the next request
-      first += places * prm.Hk * prm.row_tiles;
-      nb = request_blocks(prm, ++b);
+    if (x >= first + places * units) {                           // on to the next request
+      first += places * units;
+      nb = req.blocks(++b);
       continue;
     }
     const long long in = (x - first) / places;                   // unit within the request
@@ -581,7 +596,7 @@ __global__ void __launch_bounds__(kWarps * 32, resident<T>(NT)) cache_attn_rows_
     const int p1 = static_cast<int>(min(places, p0 + (stop - x)));
     const int blk0 = max(p0 - kPieceCost, 0), blk1 = p1 - kPieceCost;
     if (blk1 > blk0) {
-      const long long unit = static_cast<long long>(b) * prm.Hk * prm.row_tiles + in;
+      const long long unit = b * units + in;
       // a share has at most one piece that goes on with a unit, and one that a later share goes on with
       const long long slot = blk0 == 0 && blk1 == nb ? -1 : 2LL * blockIdx.x + (blk0 == 0);
       if (!attend_piece<T, D, NT>(par, smem, sh, into, from, unit, cache_len(prm, b), blk0, blk1, slot)) return;
@@ -607,11 +622,12 @@ __global__ void __launch_bounds__(kJoinWarps * 32) cache_attn_rows_join_kernel(c
   const long long bh = row / prm.R;
   const int r = static_cast<int>(row - bh * prm.R);
   const int b = static_cast<int>(bh / prm.Hk);
-  const Share share = work_share(prm, lane);
-  const int nb = request_blocks(prm, b);
+  Requests req(prm, lane);
+  const Share share = work_share(prm, req);
+  const int nb = req.blocks(b);
   const int tile_rows = 8 * row_columns<T>(prm.R);
   const long long unit = bh * prm.row_tiles + r / tile_rows;
-  const long long first = places_before(prm, b, lane) * prm.Hk * prm.row_tiles +
+  const long long first = req.before(b) * prm.Hk * prm.row_tiles +
                           (unit - static_cast<long long>(b) * prm.Hk * prm.row_tiles) * unit_places(nb) + kPieceCost;
   // shares that hold a piece of the unit
   const long long p0 = first / share.size, p1 = (first + nb - 1) / share.size;

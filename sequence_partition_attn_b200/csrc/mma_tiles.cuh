@@ -23,7 +23,8 @@ __device__ __forceinline__ int box_row(int t, int s0, int s1) {
   return (t + kRows > s1 && s1 - kRows >= s0) ? s1 - kRows : t;
 }
 
-__device__ __forceinline__ int count_tiles(const AttnTables& t, int g) {
+template <typename Tables>
+__device__ __forceinline__ int count_tiles(const Tables& t, int g) {
   int n = 0;
   for (int p = 0; p < t.P;) {
     int s0, s1;
@@ -34,10 +35,11 @@ __device__ __forceinline__ int count_tiles(const AttnTables& t, int g) {
 }
 
 // Walks the 128-row tiles of the ranges that group g streams.
+template <typename Tables>
 struct TileWalk {
-  const AttnTables& t;
+  const Tables& t;
   int g, p, s0, s1, at;
-  __device__ __forceinline__ TileWalk(const AttnTables& tab, int group) : t(tab), g(group), p(0), s0(0), s1(0), at(0) {
+  __device__ __forceinline__ TileWalk(const Tables& tab, int group) : t(tab), g(group), p(0), s0(0), s1(0), at(0) {
     advance_range();
   }
   __device__ __forceinline__ void advance_range() {

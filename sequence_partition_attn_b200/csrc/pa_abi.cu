@@ -697,13 +697,20 @@ static int fill_owner_tiles(pa::AttnTables& t, int tile_rows) {
   return acc;
 }
 
+}  // extern "C"
+
 // Launch order of the bf16 backward pass's units: groups that stream the most tokens first (ties in
 // group order), all heads and tiles of a group together, which share what they stream.
-static bool fill_units(pa::BwdSide& side, long long BH) {
-  const pa::AttnTables& t = side.t;
+template <int MP>
+static bool fill_units(pa::BwdSide<MP>& side, const pa::AttnTables& t, long long BH) {
   const int tile = pa::attn_bwd_tc_tile_rows();
-  long long tokens[PA_MAX_P];
+  side.P = t.P;
+  side.QG = t.QG;
+  memcpy(side.part_off, t.part_off, sizeof(int) * (t.P + 1));
+  memcpy(side.qg_row0, t.qg_row0, sizeof(int) * (t.QG + 1));
+  long long tokens[MP];
   for (int g = 0; g < t.QG; ++g) {
+    memcpy(side.fresh_bits[g], t.fresh_bits[g], sizeof side.fresh_bits[g]);
     tokens[g] = 0;
     for (int p = 0; p < t.P; ++p)
       if (pa::fresh_bit(t.fresh_bits, g, p)) tokens[g] += t.part_off[p + 1] - t.part_off[p];
@@ -722,6 +729,35 @@ static bool fill_units(pa::BwdSide& side, long long BH) {
   side.units = static_cast<int>(acc);
   return true;
 }
+
+template <int MP>
+static int launch_backward_tc(pa_ctx* ctx, const pa_attn_bwd_desc* d, const pa::AttnTables& tk, const pa::AttnTables& tq,
+                              cudaStream_t st) {
+  const long long BH = static_cast<long long>(d->B) * d->H;
+  pa::BwdTcParams<MP> tc;
+  int rc;
+  if ((rc = encode_qkv_map(ctx, &tc.tm_q, d->q, (int)BH, d->N, d->D))) return rc;
+  if ((rc = encode_qkv_map(ctx, &tc.tm_k, d->k, (int)BH, d->N, d->D))) return rc;
+  if ((rc = encode_qkv_map(ctx, &tc.tm_v, d->v, (int)BH, d->N, d->D))) return rc;
+  if ((rc = encode_qkv_map(ctx, &tc.tm_do, d->dout, (int)BH, d->N, d->D))) return rc;
+  tc.lse = d->lse;
+  tc.delta = d->delta;
+  tc.dq = d->dq;
+  tc.dk = d->dk;
+  tc.dv = d->dv;
+  tc.status = ctx->d_status;
+  tc.N = d->N;
+  tc.scale = d->scale;
+  tc.scale_log2 = d->scale * 1.4426950408889634f;
+  if (!fill_units(tc.kv, tk, BH) || !fill_units(tc.q, tq, BH) || tc.kv.units > 0x7fffffff - tc.q.units)
+    return fail(ctx, PA_EINVAL, "too many work units");
+  int e = pa::launch_delta(d->o, d->dout, d->dlse, d->delta, BH * d->N, d->D, d->dtype, st);
+  if (e) return cuda_fail(ctx, e, "delta launch");
+  e = pa::launch_attn_bwd_tc(tc, d->D, st);
+  return e ? cuda_fail(ctx, e, "attention backward launch") : PA_OK;
+}
+
+extern "C" {
 
 static int pa_attn_backward_impl(pa_ctx* ctx, const pa_attn_bwd_desc* d, void* stream) {
   if (!ctx) return fail(nullptr, PA_EINVAL, "ctx is NULL");
@@ -787,28 +823,7 @@ static int pa_attn_backward_impl(pa_ctx* ctx, const pa_attn_bwd_desc* d, void* s
     e = pa::launch_attn_bwd_fma(prm, own, st);
     return e ? cuda_fail(ctx, e, "attention backward launch") : PA_OK;
   }
-  pa::BwdTcParams tc;
-  if ((rc = encode_qkv_map(ctx, &tc.tm_q, d->q, (int)BH, d->N, d->D))) return rc;
-  if ((rc = encode_qkv_map(ctx, &tc.tm_k, d->k, (int)BH, d->N, d->D))) return rc;
-  if ((rc = encode_qkv_map(ctx, &tc.tm_v, d->v, (int)BH, d->N, d->D))) return rc;
-  if ((rc = encode_qkv_map(ctx, &tc.tm_do, d->dout, (int)BH, d->N, d->D))) return rc;
-  tc.lse = d->lse;
-  tc.delta = d->delta;
-  tc.dq = d->dq;
-  tc.dk = d->dk;
-  tc.dv = d->dv;
-  tc.status = ctx->d_status;
-  tc.N = d->N;
-  tc.scale = d->scale;
-  tc.scale_log2 = d->scale * 1.4426950408889634f;
-  tc.kv.t = tk;
-  tc.q.t = tq;
-  if (!fill_units(tc.kv, BH) || !fill_units(tc.q, BH) || tc.kv.units > 0x7fffffff - tc.q.units)
-    return fail(ctx, PA_EINVAL, "too many work units");
-  e = pa::launch_delta(d->o, d->dout, d->dlse, d->delta, rows, d->D, d->dtype, st);
-  if (e) return cuda_fail(ctx, e, "delta launch");
-  e = pa::launch_attn_bwd_tc(tc, d->D, st);
-  return e ? cuda_fail(ctx, e, "attention backward launch") : PA_OK;
+  return d->P <= 32 ? launch_backward_tc<32>(ctx, d, tk, tq, st) : launch_backward_tc<PA_MAX_P>(ctx, d, tk, tq, st);
 }
 
 static int pa_cache_store_impl(pa_ctx* ctx, const pa_cache_store_desc* d, void* stream) {

@@ -382,14 +382,21 @@ struct BwdParams {
 };
 
 // Owners of row tiles in the bf16 backward pass: their groups with the partitions they stream, and
-// the launch order of the units (group, head, tile): groups with the most to stream first.
+// the launch order of the units (group, head, tile): groups with the most to stream first.  Sized
+// by the number of partitions, up to 32 or up to PA_MAX_P: the parameters of a launch are then 1.5
+// or 7 KB, and the smaller launch is microseconds sooner on its way.
+template <int MP>
 struct BwdSide {
-  AttnTables t;
-  int units;
-  int unit_start[PA_MAX_P + 1];   // by place in the order
-  uint8_t order[PA_MAX_P];
+  static constexpr int kWords = MP / 32;
+  int P, QG, units;
+  int part_off[MP + 1];
+  int qg_row0[MP + 1];
+  int unit_start[MP + 1];         // by place in the order
+  uint32_t fresh_bits[MP][kWords];
+  uint8_t order[MP];
 };
 
+template <int MP>
 struct BwdTcParams {
   CUtensorMap tm_q, tm_k, tm_v, tm_do;
   const float* lse;
@@ -400,7 +407,7 @@ struct BwdTcParams {
   int* status;
   int N;
   float scale, scale_log2;
-  BwdSide kv, q;
+  BwdSide<MP> kv, q;
 };
 
 struct CacheStoreParams {
@@ -460,13 +467,15 @@ __device__ __forceinline__ void e4m3_to_f16(uint32_t codes, uint32_t& lo, uint32
 
 // The maximal run of selected partitions at or after `from` that holds tokens, as the token
 // range [s0, s1) (neighbouring partitions join); returns where to go on.  s0 == s1 at the end.
-__device__ __forceinline__ int next_range(const AttnTables& t, int g, int from, int& s0, int& s1) {
+template <typename Tables>
+__device__ __forceinline__ int next_range(const Tables& t, int g, int from, int& s0, int& s1) {
   s0 = s1 = 0;
   int p = from;
-  while (p < t.P && !(fresh_bit(t.fresh_bits, g, p) && t.part_off[p + 1] > t.part_off[p])) ++p;
+  auto selected = [&](int i) { return (t.fresh_bits[g][i >> 5] >> (i & 31)) & 1u; };
+  while (p < t.P && !(selected(p) && t.part_off[p + 1] > t.part_off[p])) ++p;
   if (p == t.P) return p;
   s0 = t.part_off[p];
-  while (p < t.P && (fresh_bit(t.fresh_bits, g, p) || t.part_off[p + 1] == t.part_off[p])) ++p;
+  while (p < t.P && (selected(p) || t.part_off[p + 1] == t.part_off[p])) ++p;
   s1 = t.part_off[p];
   return p;
 }

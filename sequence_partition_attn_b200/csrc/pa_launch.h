@@ -39,7 +39,8 @@ int launch_delta(const void* o, const void* dout, const float* dlse, float* delt
 int launch_attn_bwd_fma(const BwdParams& prm, int own_rows, cudaStream_t st);     // own_rows 32 or 64
 
 int attn_bwd_tc_tile_rows();
-int launch_attn_bwd_tc(const BwdTcParams& prm, int D, cudaStream_t st);
+int launch_attn_bwd_tc(const BwdTcParams<32>& prm, int D, cudaStream_t st);
+int launch_attn_bwd_tc(const BwdTcParams<PA_MAX_P>& prm, int D, cudaStream_t st);
 
 int launch_cache_store(const CacheStoreParams& prm, unsigned blocks, int dtype, int D, cudaStream_t st);
 
