@@ -4,12 +4,16 @@
 // Bound by the tensor cores and the exponentials, as the bf16 partition attention (attn_tc.cu),
 // whose scheme of two 128-row query tiles per CTA it follows: S = Q K^T and O += P V on tcgen05,
 // P written to TMEM over S.  What differs is where K and V come from: a warpgroup reads the codes
-// of each 128-token tile, two cache blocks, with plain 16-byte loads (the next item's loads in
-// flight), multiplies them by the block's scale in fp32 and writes bf16 to the swizzled tile that
-// the products read.  The scale is a power of two, so code * scale is exact in bf16: nothing is
+// of each 128-token tile, two cache blocks, with asynchronous copies a whole tile of K and V ahead,
+// multiplies them by the block's scale in fp32 and writes bf16 to the swizzled tile that the
+// products read.  The scale is a power of two, so code * scale is exact in bf16: nothing is
 // rounded that the cache did not round already, and the scores need no scale of their own.
 // The codes cross HBM and L2 in 8 bits; a pass that widened the cache to bf16 first would write
-// and read it again at twice the size.
+// and read it again at twice the size.  24 heads x 9450 queries x 18900 tokens, D = 128: 1.56 ms, a
+// tile of 128 tokens every 3800 cycles, of which the softmax warps work 2200 and wait for the
+// products between.  (Loads into registers one block ahead: 1.93 ms, as L2 answers in about a
+// thousand cycles and a tile has four of them in a row.  f16 tiles with the scales in the softmax
+// instead: fewer instructions to widen, but 500 more per tile in the softmax, which sets the pace.)
 //
 // Roles (512 threads, one CTA per SM; 128 registers at launch, then 80 / 176 / 176 / 80):
 //   warp 0      loads Q_a, Q_b by TMA.     warp 1  TMEM owner and MMA issuer.
@@ -41,8 +45,9 @@ struct Layout {
   static constexpr int kQ = 0;                                 // Q_a, Q_b
   static constexpr int kK = kQ + 2 * kTile;
   static constexpr int kV = kK + kStages * kTile;
-  static constexpr int kML = kV + kStages * kTile;             // (max, sum) per row: [tile][row]
-  static constexpr int kBar = kML + 2 * kBM * 8;
+  static constexpr int kItem = 64 * D;                         // codes of a cache block
+  static constexpr int kCodes = kV + kStages * kTile;          // the next four items
+  static constexpr int kBar = kCodes + 4 * kItem;
   enum { Q_FULL = 0, K_FULL = 1, V_FULL = K_FULL + kStages, K_EMPTY = V_FULL + kStages,
          V_EMPTY = K_EMPTY + kStages, S_FULL = V_EMPTY + kStages, P_LO = S_FULL + 2, P_HI = P_LO + 2,
          O_FINAL = P_HI + 2, ML_FULL = O_FINAL + 2, NBAR = ML_FULL + 2 };
@@ -95,28 +100,31 @@ __device__ __forceinline__ void widen(uint32_t codes, float2 scale, uint32_t& lo
   hi = pack_bf16x2(y.x, y.y);
 }
 
-// One item of the widening warpgroup: a cache block (64 tokens) of K or of V, 16-byte pieces.
+// One item of the widening warpgroup: a cache block (64 tokens) of K or of V in 16-byte pieces.
+// A thread copies the pieces that it widens itself, so its own wait is all that a copy needs.
 template <int D>
 struct Item {
   static constexpr int kSegs = D / 16;                 // 16-code pieces per token
   static constexpr int kPieces = 64 * kSegs / 128;     // per thread
-  uint4 c[kPieces];
-  float scale;
 
-  // Tokens at or behind `end` are not read and become 0.
-  __device__ __forceinline__ void load(const uint8_t* codes, const float* scales, int tok, int end, int thread) {
-    scale = tok < end ? __ldg(scales + tok / PA_CACHE_BLOCK) : 0.0f;
+  // Starts the copies; tokens at or behind `end` are not read and become 0.
+  static __device__ __forceinline__ void fetch(uint32_t slot, const uint8_t* codes, int tok, int end, int thread) {
 #pragma unroll
     for (int n = 0; n < kPieces; ++n) {
       const int i = n * 128 + thread;
       const int j = tok + i / kSegs;
-      c[n] = make_uint4(0u, 0u, 0u, 0u);
-      if (j < end) c[n] = __ldg(reinterpret_cast<const uint4*>(codes + static_cast<size_t>(j) * D + (i % kSegs) * 16));
+      const bool in = j < end;
+      const uint8_t* src = codes + (in ? static_cast<size_t>(j) * D + (i % kSegs) * 16 : 0);
+      asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(slot + i * 16), "l"(src), "r"(in ? 16 : 0) : "memory");
     }
+    asm volatile("cp.async.commit_group;" ::: "memory");
   }
 
   // Into rows `row0` .. of a swizzled tile: 16-byte chunk c of row r lies at chunk c ^ (r & 7).
-  __device__ __forceinline__ void store(uint8_t* tile, int row0, int thread) const {
+  static __device__ __forceinline__ void store(const uint8_t* slot, float scale, uint8_t* tile, int row0, int thread) {
+    uint4 c[kPieces];
+#pragma unroll
+    for (int n = 0; n < kPieces; ++n) c[n] = *reinterpret_cast<const uint4*>(slot + (n * 128 + thread) * 16);
 #pragma unroll
     for (int n = 0; n < kPieces; ++n) {
       const int i = n * 128 + thread;
@@ -301,7 +309,8 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attn_tc_kernel(const __grid
       const float2 a = __fadd2_rn(__fadd2_rn(acc[0], acc[1]), __fadd2_rn(acc[2], acc[3]));
       l += a.x + a.y;
       if (j == T - 1) {
-        reinterpret_cast<float2*>(gbase + L::kML)[x * kBM + row] = make_float2(m, l);
+        // over Q_x, whose last product is done
+        reinterpret_cast<float2*>(gbase + L::kQ + x * L::kTile)[row] = make_float2(m, l);
         mbar_arrive(bar(L::ML_FULL + x));
       }
     }
@@ -314,35 +323,42 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attn_tc_kernel(const __grid
     const float* scales[2] = {prm.k_scale + static_cast<size_t>(bh) * prm.blocks,
                               prm.v_scale + static_cast<size_t>(bh) * prm.blocks};
     bool ok = true;
-    Item<D> cur;
-    if (T > 0) cur.load(codes[0], scales[0], begin, end, thread);
+    // item i of a tile: block i & 1 of K (i < 2) or V
+    auto fetch = [&](int i, int tok) {
+      Item<D>::fetch(base + L::kCodes + i * L::kItem, codes[i >> 1], tok + (i & 1) * 64, end, thread);
+    };
+    auto scale_of = [&](int i, int tok) {
+      return tok + (i & 1) * 64 < end ? __ldg(scales[i >> 1] + tok / PA_CACHE_BLOCK + (i & 1)) : 0.0f;
+    };
+    float scale[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      fetch(i, begin);
+      scale[i] = scale_of(i, begin);
+    }
     for (int j = 0; ok && j < T; ++j) {
       const int s = j % kStages;
       const int tok = begin + j * kBN;
 #pragma unroll
-      for (int kv = 0; kv < 2; ++kv) {
-        if (j >= kStages &&
+      for (int i = 0; i < 4; ++i) {
+        const int kv = i >> 1;
+        if ((i & 1) == 0 && j >= kStages &&
             !mbar_wait(bar((kv ? L::V_EMPTY : L::K_EMPTY) + s), (j / kStages - 1) & 1, abort_flag, status)) {
           ok = false;
           break;
         }
-        uint8_t* tile = gbase + (kv ? L::kV : L::kK) + s * L::kTile;
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          Item<D> nxt;
-          if (h == 0)
-            nxt.load(codes[kv], scales[kv], tok + 64, end, thread);
-          else if (kv == 0)
-            nxt.load(codes[1], scales[1], tok, end, thread);
-          else
-            nxt.load(codes[0], scales[0], tok + kBN, end, thread);
-          cur.store(tile, h * 64, thread);
-          cur = nxt;
+        asm volatile("cp.async.wait_group 3;" ::: "memory");
+        Item<D>::store(gbase + L::kCodes + i * L::kItem, scale[i], gbase + (kv ? L::kV : L::kK) + s * L::kTile,
+                       (i & 1) * 64, thread);
+        fetch(i, tok + kBN);
+        scale[i] = scale_of(i, tok + kBN);
+        if (i & 1) {
+          fence_async_smem();
+          mbar_arrive(bar((kv ? L::V_FULL : L::K_FULL) + s));
         }
-        fence_async_smem();
-        mbar_arrive(bar((kv ? L::V_FULL : L::K_FULL) + s));
       }
     }
+    asm volatile("cp.async.wait_all;" ::: "memory");
     const int row = (warp & 3) * 32 + lane;
     const uint32_t lane_off = static_cast<uint32_t>((warp & 3) * 32) << 16;
     for (int x = 0; ok && x < nx; ++x) {
@@ -355,7 +371,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attn_tc_kernel(const __grid
             !mbar_wait(bar(L::ML_FULL + x), 0, abort_flag, status))
           break;
         tc_fence_after();
-        ml = reinterpret_cast<const float2*>(gbase + L::kML)[x * kBM + row];
+        ml = reinterpret_cast<const float2*>(gbase + L::kQ + x * L::kTile)[row];
       }
       const float inv = 1.0f / ml.y;
 #pragma unroll 1
