@@ -867,8 +867,15 @@ static int pa_cache_store_impl(pa_ctx* ctx, const pa_cache_store_desc* d, void* 
   return e ? cuda_fail(ctx, e, "cache store launch") : PA_OK;
 }
 
-// bf16 queries take the tcgen05 kernel when a KV head has more than this many query rows.
-static bool cache_attn_many_rows(pa_dtype dtype, long long rows) { return dtype == PA_BF16 && rows > 64; }
+// bf16 queries take the tcgen05 kernel when a KV head has more than 32 query rows: it reads the codes
+// once for 256 rows, but takes 128-token tiles and 128 rows at the least, the other reads them once
+// for every 16 rows and wastes less on few.  us on a B200, D = 128, other kernel against tcgen05:
+//   rows                               16         32         48         64        128
+//   24 heads,  1 x 4096 tokens     17.4/22.3  21.5/22.1  26.8/22.4  30.3/22.1  46.6/23.7
+//    8 heads,  8 x 2048 tokens     20.5/24.2  25.0/24.2  30.5/24.6  36.1/24.4  59.8/27.2
+//    2 heads, 1 x 16384 tokens     14.2/26.0  16.5/25.7  18.3/25.9  18.9/23.1  23.9/27.6
+// (the last: so many splits that joining them costs as much as the attention).
+static bool cache_attn_many_rows(pa_dtype dtype, long long rows) { return dtype == PA_BF16 && rows > 32; }
 
 // Sizes and the split of the token axis of pa_cache_attn: a rule on sizes alone, so that the
 // scratch can be sized beforehand and a captured call replays with other lengths.
