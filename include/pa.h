@@ -345,10 +345,11 @@ typedef struct {
 
 /* Attention state of each query row against the first lens[b] tokens of its request's cache:
  *   lse_i = ln sum_j exp(scale q_i . k_j),  o_i = sum_j exp(scale q_i . k_j - lse_i) v_j.
- * Query head h reads KV head h / (H / Hk).  Tokens at or behind lens[b] and the scales of blocks
- * behind it have no influence, whatever they hold; without any token o = 0, lse = -inf.  With P = 1 the result has the
- * layout of pa_partition_attn's states, so pa_merge_states joins it with others.  The scratch
- * belongs to the caller: calls that may overlap need one each.  A length outside [0, M] is
+ * Query head h reads KV head h / (H / Hk).  The scales are powers of two or 0, as pa_cache_store
+ * leaves them.  Tokens at or behind lens[b] and the scales of blocks behind it have no influence,
+ * whatever they hold; without any token o = 0, lse = -inf.  The result has the layout of one of
+ * pa_partition_attn's states, so pa_merge_states joins it with others.  The scratch belongs to
+ * the caller: calls that may overlap need one each.  A length outside [0, M] is
  * clamped and records PA_EINVAL in the context's status word.  Results do not depend on the
  * order in which blocks run.  Errors: PA_EINVAL, PA_EALIGN, PA_EUNSUPPORTED, PA_ECUDA. */
 int pa_cache_attn(pa_ctx* ctx, const pa_cache_attn_desc* desc, void* stream);

@@ -12,7 +12,9 @@ GPU and NCCL moving the data (over NVLink / NVSwitch):
   KV blocks circulate, each rank computes the states of its own queries against the block
   it holds while the next block is in transfer, and the g blocks' states are merged into
   the group state (DiTango web summary, Methodology 2, "Group-wise state computation":
-  g - 1 KV transfers overlapped with the attention, yielding a composed group state).
+  g - 1 KV transfers overlapped with the attention, yielding a composed group state).  With
+  ``kv_bits=8`` the blocks circulate as 8-bit codes with a scale per 64 tokens and head:
+  half the bytes on the links, and one extra rounding of K and V.
 
 Every peer block is received into this GPU's own memory before a kernel reads it; no
 kernel reads another GPU's memory.
@@ -30,8 +32,8 @@ import numpy as np
 import torch
 import torch.distributed as dist
 
-from . import (Context, pa_merge_states, pa_partition_attn, pa_relayout_seq2head,
-               pa_relayout_seq2head_at)
+from . import (PA_CACHE_BLOCK, Context, cache_attn_workspace, pa_cache_attn, pa_cache_store,
+               pa_merge_states, pa_partition_attn, pa_relayout_seq2head, pa_relayout_seq2head_at)
 
 
 # ------------------------------------------------------------------ kernel launches
@@ -52,6 +54,17 @@ class DeviceOps:
 
     def attend(self, q, k, v, part_off, G, fresh, o_part, lse_part, stream=None):
         pa_partition_attn(self.ctx, q, k, v, part_off, G, fresh, o_part, lse_part, stream=stream)
+
+    def store(self, k, v, cache, stream=None):
+        """Round k, v [1, H, M, D] into cache = (k codes, v codes, k scales, v scales)."""
+        pa_cache_store(self.ctx, k, v, None, *cache, stream=stream)
+
+    def cache_workspace(self, q, cache):
+        return cache_attn_workspace(self.ctx, q, cache[0])
+
+    def attend_cache(self, q, cache, o, lse, workspace, stream=None):
+        """State of q against all tokens of the 8-bit cache."""
+        pa_cache_attn(self.ctx, q, *cache, None, o, lse, workspace=workspace, stream=stream)
 
     def merge(self, part_off, G, o_part, lse_part, o, lse, stream=None):
         pa_merge_states(self.ctx, part_off, G, None, o_part, lse_part, None, None, o, lse,
@@ -257,6 +270,20 @@ class TorusUlysses:
 
 
 # ------------------------------------------------------------------ ring inside a group
+def cache_bytes(H: int, N: int, D: int) -> int:
+    """Bytes of an 8-bit KV block of N tokens: K and V codes, then their scales."""
+    return 2 * H * (N * D + 4 * -(-N // PA_CACHE_BLOCK))
+
+
+def cache_views(buf, H: int, N: int, D: int):
+    """(k codes, v codes, k scales, v scales) of an 8-bit KV block in the bytes of buf."""
+    codes, scales = H * N * D, H * -(-N // PA_CACHE_BLOCK)
+    at = [0, codes, 2 * codes, 2 * codes + 4 * scales]
+    kc, vc = (buf[a:a + codes].view(1, H, N, D) for a in at[:2])
+    ks, vs = (buf[a:a + 4 * scales].view(torch.float32).view(1, H, scales // H) for a in at[2:])
+    return [kc, vc, ks, vs]
+
+
 class GroupRing:
     """Ring-composed attention inside the group of ranks `group` (DiTango web summary,
     Methodology 2, "Group-wise state computation").
@@ -267,14 +294,24 @@ class GroupRing:
     that block moves on to rank r + 1 and the next one arrives from rank r - 1 (g - 1
     transfers, each overlapped with a step's attention); the g * P_blk states, ordered by
     token, are then merged into the group state (O, LSE) of its queries.
+
+    ``kv_bits=8``: each rank rounds its KV block into an 8-bit cache once, and the codes and
+    scales circulate (one message of 2 * H * (N_blk * D + 4 * ceil(N_blk / 64)) bytes per step
+    instead of two of H * N_blk * D elements); every block, the rank's own one too, is read
+    from its codes, so all ranks see the same K and V.  A block is one state then: P_blk = 1.
     """
 
     def __init__(self, ops, exchange, group, N_blk, H, D, P_blk, dtype=torch.bfloat16,
-                 device="cuda:0"):
+                 device="cuda:0", kv_bits=None):
         self.ops, self.ex, self.group = ops, exchange, group
         self.rank, self.g = _rank_info(group)
         if P_blk < 1 or N_blk < 1:
             raise ValueError("empty block")
+        if kv_bits not in (None, 8):
+            raise ValueError(f"kv_bits={kv_bits}: None (blocks in dtype) or 8")
+        if kv_bits == 8 and P_blk != 1:
+            raise ValueError(f"a block of 8-bit K and V is one state: P_blk={P_blk}")
+        self.kv_bits = kv_bits
         self.N_blk, self.H, self.D, self.P_blk = N_blk, H, D, P_blk
         S = -(-N_blk // P_blk)
         self.blk_off = np.array([min(p * S, N_blk) for p in range(P_blk + 1)], dtype=np.int32)
@@ -284,12 +321,18 @@ class GroupRing:
         self.merge_off[-1] = N_blk
         dev = torch.device(device)
         mk = lambda *s, dt=dtype: torch.empty(*s, dtype=dt, device=dev)     # noqa: E731
-        self.kv = [[mk(1, H, N_blk, D), mk(1, H, N_blk, D)] for _ in range(2)]
+        if kv_bits == 8:
+            # own block, then the two that blocks arrive in: each one run of bytes
+            self.wire = [[mk(cache_bytes(H, N_blk, D), dt=torch.uint8)] for _ in range(3)]
+            self.kv = [cache_views(w[0], H, N_blk, D) for w in self.wire]
+        else:
+            self.kv = [[mk(1, H, N_blk, D), mk(1, H, N_blk, D)] for _ in range(2)]
         self.o_part = mk(P, 1, H, N_blk, D)
         self.lse_part = mk(P, 1, H, N_blk, dt=torch.float32)
         self.o = mk(1, H, N_blk, D)
         self.lse = mk(1, H, N_blk, dt=torch.float32)
         self.cuda = dev.type == "cuda"
+        self.workspace = ops.cache_workspace(self.o, self.kv[0]) if kv_bits == 8 else None
         if self.cuda:
             self.s_comm = torch.cuda.Stream(device=dev)
 
@@ -303,23 +346,29 @@ class GroupRing:
         prv_g = dist.get_global_rank(self.group, prv) if self.group is not None else prv
         cur = torch.cuda.current_stream() if self.cuda else None
         comm = self.s_comm if self.cuda else None
-        blk = [k, v]
-        done = None                            # event: attention on the previous block issued
+        eight = self.kv_bits == 8
+        if eight:
+            blk, send, into, held = self.kv[0], self.wire[0], self.wire[1:], self.kv[1:]
+            self.ops.store(k, v, blk, stream=cur)
+        else:
+            blk = send = [k, v]
+            into = held = self.kv
         for s in range(g):
             src = (r - s) % g
             work = None
             if s < g - 1:
-                dst_buf = self.kv[s % 2]
                 if self.cuda:
                     comm.wait_stream(cur)      # the block to send is complete; recv buffer free
-                work = self.ex.ring(blk, dst_buf, nxt_g, prv_g, stream=comm)
-            self.ops.attend(q, blk[0], blk[1], self.blk_off, Pb, None,
-                            self.o_part[src * Pb:(src + 1) * Pb], self.lse_part[src * Pb:(src + 1) * Pb],
-                            stream=cur)
+                work = self.ex.ring(send, into[s % 2], nxt_g, prv_g, stream=comm)
+            o, lse = self.o_part[src * Pb:(src + 1) * Pb], self.lse_part[src * Pb:(src + 1) * Pb]
+            if eight:
+                self.ops.attend_cache(q, blk, o[0], lse[0], self.workspace, stream=cur)
+            else:
+                self.ops.attend(q, blk[0], blk[1], self.blk_off, Pb, None, o, lse, stream=cur)
             if s < g - 1:
                 if work is not None:
                     self.ex.wait(work, stream=cur)   # the next block has arrived
-                blk = self.kv[s % 2]
+                blk, send = held[s % 2], into[s % 2]
         self.ops.merge(self.merge_off, g * Pb, self.o_part, self.lse_part, self.o, self.lse, stream=cur)
         return self.o, self.lse
 

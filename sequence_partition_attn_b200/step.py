@@ -16,7 +16,7 @@ from __future__ import annotations
 import numpy as np
 import torch
 
-from . import (Context, pa_merge_states, pa_partition_attn, pa_relayout_seq2head,
+from . import (Context, pa_attn_backward, pa_merge_states, pa_partition_attn, pa_relayout_seq2head,
                pa_state_drift, predict_fresh, select_fresh)
 
 
@@ -64,6 +64,7 @@ class AttentionStep:
         self.lse_cached = mk(P, B, H, N, dt=torch.float32) if reuse else None
         self.o, self.lse = mk(B, H, N, D), mk(B, H, N, dt=torch.float32)
         self.w = mk(self.QG, P, dt=torch.float32)
+        self.delta = mk(B, H, N, dt=torch.float32)      # scratch of the backward pass
         self.flops = attn_flops(self.part_off, G, self.fresh, B, H, D)
         self.merge_bytes = merge_bytes(B, H, N, D, P, torch.empty(0, dtype=dtype).element_size())
 
@@ -89,6 +90,16 @@ class AttentionStep:
     def run(self, stream=None):
         self.attention(stream)
         self.merge(stream)
+
+    def backward(self, do, dq, dk, dv, dlse=None, stream=None, q=None, k=None, v=None, o=None, lse=None):
+        """Gradients dq, dk, dv of the loss by q, k, v through the fresh pairs, given its
+        gradients do by o and dlse by lse (None: 0).  Reads o and lse as ``run`` left them (all
+        five default to the step's own buffers).  Cached states count as constants: they hold
+        no K and V to pass a gradient to.  Uses the step's scratch: one backward at a time."""
+        pick = lambda given, own: own if given is None else given            # noqa: E731
+        pa_attn_backward(self.ctx, pick(q, self.q), pick(k, self.k), pick(v, self.v),
+                         pick(o, self.o), pick(lse, self.lse), do, self.part_off, self.G, self.fresh,
+                         dq, dk, dv, self.delta, dlse=dlse, stream=stream)
 
 
 class StreamedSteps:
