@@ -49,143 +49,93 @@ __global__ void __launch_bounds__(256) delta_kernel(const T* __restrict__ o, con
   if (row < rows && c == 0) delta[row] = sum - (dlse ? dlse[row] : 0.0f);
 }
 
-// ------------------------------------------------------------------ FMA kernels
-// A block owns kOwn rows (queries for dQ, keys for dK and dV) and streams tiles of 64 rows of the
-// other side through shared memory.  Products run on packed pairs of fp32 (two multiply-adds per
-// instruction: the multiply-add pipe, not the issue slots, is then what bounds them); pairs run
-// along the summed index in the first products and along the channels in the second.
-constexpr int kT = 64;               // streamed rows per tile
-constexpr int kThreads = 256;        // 16 x 16
+// ------------------------------------------------------------------ fp32 on the tensor cores
+// An fp32 value is a sum of three bf16 ones: x = x0 + x1 + x2 with x0 its upper half (cut, so that it
+// cannot overflow), x1 the rest rounded and x2 what is left, off by 2^-25 of x.  A product of two values takes
+// the six terms x0y0, x0y1, x1y0, x1y1, x0y2, x2y0; the others are below 2^-22 of it, and the sums
+// are fp32.  That is six bf16 products for one, at the tensor cores' rate.
+//
+// A block owns kOwn rows and streams tiles of the other side; its 8 warps are kOwn / 16 groups of
+// 16 own rows times kT / 16 groups of 16 streamed rows.  With A the own and B the streamed rows,
+//   dK, dV (own K, V; stream Q, dO):  S^T = K Q^T, dP^T = V dO^T, dK += dS^T Q, dV += P^T dO
+//   dQ     (own Q, dO; stream K, V):  S = Q K^T, dP = dO V^T, dQ += dS K
+// so both are X = A0 B0^T, Y = A1 B1^T, acc0 += dS(X, Y) B0, acc1 += P(X) B1.  X and Y leave the
+// products in the layout in which P and dS enter the next ones.  The groups of streamed rows sum
+// into accumulators of their own, joined in order at the end.
+constexpr int kThreads = 256;
 
 template <int D, int kOwn>
-struct Smem {
-  static constexpr int kRow = D + 4;       // 16-byte reads of 8 rows then fall in different banks
-  static constexpr int kOwnTile = kOwn * kRow;
-  static constexpr int kTile = kT * kRow;
-  static constexpr int kPRow = kOwn + 4;   // weights [streamed row][own row]
-  static constexpr int kP = kT * kPRow;
-  static constexpr int kBytes = (2 * kOwnTile + 2 * kTile + 2 * kP + 2 * kT) * 4;
+struct Shape {
+  static constexpr int kRowGroups = kOwn / 16, kStrGroups = 8 / kRowGroups;
+  static constexpr int kT = 16 * kStrGroups;         // streamed rows per tile
+  static constexpr int kRow = 2 * D;                 // bytes; 16-byte chunk c of row r lies at chunk c ^ (r & 7)
+  static constexpr int kOwnPlane = kOwn * kRow, kStrPlane = kT * kRow;
+  static constexpr int kOwnAt = 0;                   // [tensor][plane][row][D] bf16
+  static constexpr int kStrAt = kOwnAt + 6 * kOwnPlane;
+  static constexpr int kRawAt = kStrAt + 6 * kStrPlane;      // the next tile, [tensor][row][D] fp32
+  static constexpr int kStatAt = kRawAt + 2 * kT * D * 4;    // lse, delta by streamed row
+  static constexpr int kBytes = kStatAt + 2 * kT * 4;
+  static_assert((kStrGroups - 1) * 2 * kOwn * D * 4 <= kStatAt - kStrAt, "the join reuses the streamed tiles");
 };
 
-// Rows [r0, r0 + kRows) of a [.., D] tensor into shared memory; rows at or past `end` read as 0,
-// so that nothing outside the range (which may be non-finite) reaches a product.
-template <int D, int kRows>
-__device__ __forceinline__ void load_tile(float* dst, const float* src, int r0, int end) {
-#pragma unroll 4
-  for (int i = threadIdx.x; i < kRows * D / 4; i += kThreads) {
-    const int r = i / (D / 4), c = (i % (D / 4)) * 4;
-    const float4 v = r0 + r < end ? load4(src + static_cast<size_t>(r0 + r) * D + c) : make_float4(0.f, 0.f, 0.f, 0.f);
-    *reinterpret_cast<float4*>(dst + r * (D + 4) + c) = v;
+__device__ __forceinline__ void ldmatrix(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
+}
+__device__ __forceinline__ void ldmatrix_trans(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
+}
+__device__ __forceinline__ void mma(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+// c0 += a b for columns 0..7 of b, c1 for columns 8..15; all six terms, the smallest first.
+__device__ __forceinline__ void mma_terms(float (&c0)[4], float (&c1)[4], const uint32_t (&a)[3][4], const uint32_t (&b)[3][4]) {
+  constexpr int ia[6] = {0, 2, 1, 0, 1, 0}, ib[6] = {2, 0, 1, 1, 0, 0};
+#pragma unroll
+  for (int i = 0; i < 6; ++i) {
+    mma(c0, a[ia[i]], b[ib[i]][0], b[ib[i]][1]);
+    mma(c1, a[ia[i]], b[ib[i]][2], b[ib[i]][3]);
   }
 }
 
-// The same tile in two steps: into registers, while the one before is used, and on to shared memory.
-template <int D>
-struct Ahead {
-  static constexpr int kN = kT * D / 4 / kThreads;
-  float4 v[kN];
-  __device__ __forceinline__ void load(const float* src, int r0, int end) {
-#pragma unroll
-    for (int n = 0; n < kN; ++n) {
-      const int i = n * kThreads + threadIdx.x;
-      const int r = r0 + i / (D / 4);
-      v[n] = r < end ? load4(src + static_cast<size_t>(r) * D + (i % (D / 4)) * 4) : make_float4(0.f, 0.f, 0.f, 0.f);
-    }
-  }
-  __device__ __forceinline__ void store(float* dst) const {
-#pragma unroll
-    for (int n = 0; n < kN; ++n) {
-      const int i = n * kThreads + threadIdx.x;
-      *reinterpret_cast<float4*>(dst + i / (D / 4) * (D + 4) + (i % (D / 4)) * 4) = v[n];
-    }
-  }
-};
-
-// acc[i][j] = a[RA ty + i] . b[tx + 16 j]
-template <int D, int RA, int RB>
-__device__ __forceinline__ void dot_tile(float (&acc)[RA][RB], const float* a, const float* b, int ty, int tx) {
-  float2 sum[RA][RB];
-#pragma unroll
-  for (int i = 0; i < RA; ++i)
-#pragma unroll
-    for (int j = 0; j < RB; ++j) sum[i][j] = make_float2(0.0f, 0.0f);
-#pragma unroll 4
-  for (int d = 0; d < D; d += 4) {
-    float4 x[RA], y[RB];
-#pragma unroll
-    for (int i = 0; i < RA; ++i) x[i] = *reinterpret_cast<const float4*>(a + (RA * ty + i) * (D + 4) + d);
-#pragma unroll
-    for (int j = 0; j < RB; ++j) y[j] = *reinterpret_cast<const float4*>(b + (tx + 16 * j) * (D + 4) + d);
-#pragma unroll
-    for (int i = 0; i < RA; ++i)
-#pragma unroll
-      for (int j = 0; j < RB; ++j) {
-        sum[i][j] = __ffma2_rn(make_float2(x[i].x, x[i].y), make_float2(y[j].x, y[j].y), sum[i][j]);
-        sum[i][j] = __ffma2_rn(make_float2(x[i].z, x[i].w), make_float2(y[j].z, y[j].w), sum[i][j]);
-      }
-  }
-#pragma unroll
-  for (int i = 0; i < RA; ++i)
-#pragma unroll
-    for (int j = 0; j < RB; ++j) acc[i][j] = sum[i][j].x + sum[i][j].y;
+// The three terms of two values, as bf16 pairs.
+__device__ __forceinline__ void split2(float x, float y, uint32_t& t0, uint32_t& t1, uint32_t& t2) {
+  const uint32_t xu = __float_as_uint(x), yu = __float_as_uint(y);
+  t0 = __byte_perm(xu, yu, 0x7632);
+  const float x1 = x - __uint_as_float(xu & 0xFFFF0000u), y1 = y - __uint_as_float(yu & 0xFFFF0000u);
+  t1 = pack_bf16x2(x1, y1);
+  t2 = pack_bf16x2(x1 - __uint_as_float(t1 << 16), y1 - __uint_as_float(t1 & 0xFFFF0000u));
 }
 
-// acc[i][2 c + e] += sum_t w[t][RO ty + i] * x[t][4 tx + 64 c + 2 e ..] (pairs of channels)
-template <int D, int RO>
-__device__ __forceinline__ void add_product(float2 (&acc)[RO][D / 32], const float* w, const float* x, int ty, int tx) {
-#pragma unroll 4
-  for (int t = 0; t < kT; ++t) {
-    float a[RO];
+// Eight channels of a row into its three planes.
+template <int kPlane>
+__device__ __forceinline__ void split_store(uint8_t* planes, int row_bytes, int r, int chunk, float4 a, float4 b) {
+  uint32_t t[3][4];
+  split2(a.x, a.y, t[0][0], t[1][0], t[2][0]);
+  split2(a.z, a.w, t[0][1], t[1][1], t[2][1]);
+  split2(b.x, b.y, t[0][2], t[1][2], t[2][2]);
+  split2(b.z, b.w, t[0][3], t[1][3], t[2][3]);
+  uint8_t* at = planes + r * row_bytes + ((chunk ^ (r & 7)) << 4);
 #pragma unroll
-    for (int i = 0; i < RO; i += 2) {
-      const float2 p = *reinterpret_cast<const float2*>(w + t * (16 * RO + 4) + RO * ty + i);
-      a[i] = p.x;
-      a[i + 1] = p.y;
-    }
-#pragma unroll
-    for (int c = 0; c < D / 64; ++c) {
-      const float4 b = *reinterpret_cast<const float4*>(x + t * (D + 4) + 4 * tx + 64 * c);
-#pragma unroll
-      for (int i = 0; i < RO; ++i) {
-        acc[i][2 * c] = __ffma2_rn(make_float2(a[i], a[i]), make_float2(b.x, b.y), acc[i][2 * c]);
-        acc[i][2 * c + 1] = __ffma2_rn(make_float2(a[i], a[i]), make_float2(b.z, b.w), acc[i][2 * c + 1]);
-      }
-    }
-  }
-}
-
-template <int D, int RO>
-__device__ __forceinline__ void store_tile(float* dst, const float2 (&acc)[RO][D / 32], float f, int own0, int own1, int ty, int tx) {
-#pragma unroll
-  for (int i = 0; i < RO; ++i) {
-    const int r = own0 + RO * ty + i;
-    if (r >= own1) continue;
-#pragma unroll
-    for (int c = 0; c < D / 64; ++c)
-      store4(dst + static_cast<size_t>(r) * D + 4 * tx + 64 * c,
-             make_float4(acc[i][2 * c].x * f, acc[i][2 * c].y * f, acc[i][2 * c + 1].x * f, acc[i][2 * c + 1].y * f));
-  }
+  for (int p = 0; p < 3; ++p) *reinterpret_cast<uint4*>(at + p * kPlane) = make_uint4(t[p][0], t[p][1], t[p][2], t[p][3]);
 }
 
 // kDq: the block owns queries and streams keys; else it owns keys and streams queries.
 template <int D, int kOwn, bool kDq>
-__device__ __forceinline__ void fma_unit(const BwdParams& prm, int tile, float* smem) {
-  using S = Smem<D, kOwn>;
-  constexpr int RO = kOwn / 16;                      // own rows per thread
-  constexpr int RA = kDq ? RO : kT / 16, RB = kDq ? kT / 16 : RO;
-  float* sOwn0 = smem;                               // Q | K
-  float* sOwn1 = sOwn0 + S::kOwnTile;                // dO | V
-  float* sStr0 = sOwn1 + S::kOwnTile;                // K | Q
-  float* sStr1 = sStr0 + S::kTile;                   // V | dO
-  float* sP = sStr1 + S::kTile;                      // dS | P, by streamed row
-  float* sdS = sP + S::kP;                           //      dS
-  float* sLse = sdS + S::kP;
-  float* sDelta = sLse + kT;
+__device__ __forceinline__ void bwd_unit(const BwdParams& prm, int tile, uint8_t* smem) {
+  using S = Shape<D, kOwn>;
+  constexpr int kT = S::kT;
   const AttnTables& t = kDq ? prm.tq : prm.tk;
   const int bh = blockIdx.y;
-  // A warp covers 4 x 8 of the 16 x 16 threads.
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int ty = (warp >> 1) * 4 + (lane >> 3), tx = (warp & 1) * 8 + (lane & 7);
+  const int rg = warp % S::kRowGroups, sg = warp / S::kRowGroups;
+  const int gid = lane >> 2, tig = lane & 3;
+  const uint32_t sbase = smem_u32(smem);
+  float* sLse = reinterpret_cast<float*>(smem + S::kStatAt);
+  float* sDelta = sLse + kT;
   int g = 0;
   while (g + 1 < t.QG && t.tile_start[g + 1] <= tile) ++g;
   const int own0 = t.qg_row0[g] + (tile - t.tile_start[g]) * kOwn;
@@ -195,95 +145,207 @@ __device__ __forceinline__ void fma_unit(const BwdParams& prm, int tile, float* 
   const float* k = static_cast<const float*>(prm.k) + head * D;
   const float* v = static_cast<const float*>(prm.v) + head * D;
   const float* dout = static_cast<const float*>(prm.dout) + head * D;
+  const float* own[2] = {kDq ? q : k, kDq ? dout : v};
+  const float* str[2] = {kDq ? k : q, kDq ? v : dout};
   // +inf makes every P of the row 0: rows outside the range, and rows without any key
-  auto load_stats = [&](int r0, int r1, int n) {
-    if (static_cast<int>(threadIdx.x) < n) {
-      const int r = r0 + threadIdx.x;
-      const float l = r < r1 ? prm.lse[head + r] : INFINITY;
-      sLse[threadIdx.x] = l == -INFINITY ? INFINITY : l;
-      sDelta[threadIdx.x] = r < r1 ? prm.delta[head + r] : 0.0f;
-    }
+  auto stat_lse = [&](int r, int end) {
+    const float l = r < end ? prm.lse[head + r] : INFINITY;
+    return l == -INFINITY ? INFINITY : l;
   };
-  load_tile<D, kOwn>(sOwn0, kDq ? q : k, own0, own1);
-  load_tile<D, kOwn>(sOwn1, kDq ? dout : v, own0, own1);
-  if (kDq) load_stats(own0, own1, kOwn);
 
-  float2 acc0[RO][D / 32], acc1[RO][D / 32];         // dQ | dK, dV
+  // Pieces of 8 channels; rows at or past `end` become 0, so that nothing outside the range (which
+  // may be non-finite) reaches a product.  A thread splits the pieces it copied.
+  constexpr int kPieces = kT * D / 8 / kThreads;
+  auto fetch = [&](int r0, int end) {
 #pragma unroll
-  for (int i = 0; i < RO; ++i)
+    for (int x = 0; x < 2; ++x)
 #pragma unroll
-    for (int c = 0; c < D / 32; ++c) acc0[i][c] = acc1[i][c] = make_float2(0.0f, 0.0f);
-  const float* str0 = kDq ? k : q;
-  const float* str1 = kDq ? v : dout;
+      for (int n = 0; n < kPieces; ++n) {
+        const int i = n * kThreads + threadIdx.x;
+        const int r = r0 + i / (D / 8);
+        const bool in = r < end;
+        const float* src = str[x] + (in ? static_cast<size_t>(r) * D + i % (D / 8) * 8 : 0);
+        const uint32_t dst = sbase + S::kRawAt + (x * kT * D + i * 8) * 4;
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(in ? 16 : 0) : "memory");
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst + 16), "l"(src + 4), "r"(in ? 16 : 0) : "memory");
+      }
+  };
+#pragma unroll
+  for (int x = 0; x < 2; ++x)
+    for (int i = threadIdx.x; i < kOwn * D / 8; i += kThreads) {
+      const int r = i / (D / 8), c = i % (D / 8);
+      float4 a = make_float4(0.f, 0.f, 0.f, 0.f), b = a;
+      if (own0 + r < own1) {
+        const float* src = own[x] + static_cast<size_t>(own0 + r) * D + c * 8;
+        a = load4(src);
+        b = load4(src + 4);
+      }
+      split_store<S::kOwnPlane>(smem + S::kOwnAt + x * 3 * S::kOwnPlane, S::kRow, r, c, a, b);
+    }
+  float lse_own[2] = {INFINITY, INFINITY}, delta_own[2] = {0.0f, 0.0f};    // rows gid, gid + 8 (dQ)
+  if (kDq)
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int r = own0 + rg * 16 + gid + 8 * h;
+      lse_own[h] = stat_lse(r, own1);
+      delta_own[h] = r < own1 ? prm.delta[head + r] : 0.0f;
+    }
+
+  float acc0[D / 8][4], acc1[D / 8][4];              // dQ | dK, dV
+#pragma unroll
+  for (int c = 0; c < D / 8; ++c)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) acc0[c][e] = acc1[c][e] = 0.0f;
+
+  // this lane's row and chunk in the four 8 x 8 matrices of a load: A tiles and transposed B tiles
+  // take rows 0..15 of chunk 0, then of chunk 1; B tiles chunks 0, 1 of rows 0..7, then of 8..15
+  const int swz = lane & 7;
+  const uint32_t rows_first = (swz + ((lane >> 3) & 1) * 8) * S::kRow, rows_last = (swz + (lane >> 4) * 8) * S::kRow;
+  const uint32_t xor_first = ((lane >> 4) ^ swz) << 4, xor_last = (((lane >> 3) & 1) ^ swz) << 4;
+  const uint32_t a_row = sbase + S::kOwnAt + rg * 16 * S::kRow + rows_first;
+  const uint32_t b_row = sbase + S::kStrAt + sg * 16 * S::kRow + rows_last;
+  const uint32_t w_row = sbase + S::kStrAt + sg * 16 * S::kRow + rows_first;
+
   int s0, s1;
   int p = next_range(t, g, 0, s0, s1);
   int st0 = s0;
-  Ahead<D> ahead0, ahead1;
-  if (st0 < s1) {
-    ahead0.load(str0, st0, s1);
-    ahead1.load(str1, st0, s1);
-  }
+  float lse_next = INFINITY, delta_next = 0.0f;      // of streamed row threadIdx.x of the next tile
+  auto ahead = [&]() {
+    fetch(st0, s1);
+    if (!kDq && threadIdx.x < kT) {
+      const int r = st0 + threadIdx.x;
+      lse_next = stat_lse(r, s1);
+      delta_next = r < s1 ? prm.delta[head + r] : 0.0f;
+    }
+  };
+  if (st0 < s1) ahead();
   while (st0 < s1) {
-    const int end = min(st0 + kT, s1);               // of this tile's rows
-    __syncthreads();
-    ahead0.store(sStr0);
-    ahead1.store(sStr1);
-    if (!kDq) load_stats(st0, end, kT);
-    __syncthreads();
-    const int n = end - st0;
+    asm volatile("cp.async.wait_all;" ::: "memory");
+    __syncthreads();                                 // the tile before is used up
+#pragma unroll
+    for (int x = 0; x < 2; ++x)
+#pragma unroll
+      for (int n = 0; n < kPieces; ++n) {
+        const int i = n * kThreads + threadIdx.x;
+        const float4* raw = reinterpret_cast<const float4*>(smem + S::kRawAt + (x * kT * D + i * 8) * 4);
+        split_store<S::kStrPlane>(smem + S::kStrAt + x * 3 * S::kStrPlane, S::kRow, i / (D / 8), i % (D / 8), raw[0], raw[1]);
+      }
+    if (!kDq && threadIdx.x < kT) {
+      sLse[threadIdx.x] = lse_next;
+      sDelta[threadIdx.x] = delta_next;
+    }
+    const int n = min(kT, s1 - st0);
     st0 += kT;
     if (st0 >= s1) {
       p = next_range(t, g, p, s0, s1);
       st0 = s0;
     }
-    if (st0 < s1) {
-      ahead0.load(str0, st0, s1);
-      ahead1.load(str1, st0, s1);
-    }
-    // rows of s are queries, columns keys
-    float s[RA][RB], dp[RA][RB];
-    dot_tile<D, RA, RB>(s, kDq ? sOwn0 : sStr0, kDq ? sStr0 : sOwn0, ty, tx);
-    dot_tile<D, RA, RB>(dp, kDq ? sOwn1 : sStr1, kDq ? sStr1 : sOwn1, ty, tx);
-    const int q1 = kDq ? own1 - own0 : n, k1 = kDq ? n : own1 - own0;
-#pragma unroll
-    for (int i = 0; i < RA; ++i)
-#pragma unroll
-      for (int j = 0; j < RB; ++j) {
-        const int r = RA * ty + i, c = tx + 16 * j;
-        const bool in = r < q1 && c < k1;
-        const float pij = in ? expf(fmaf(s[i][j], prm.scale, -sLse[r])) : 0.0f;
-        const float ds = in ? pij * (dp[i][j] - sDelta[r]) : 0.0f;
-        if (kDq) {
-          sP[c * S::kPRow + r] = ds;
-        } else {
-          sP[r * S::kPRow + c] = pij;
-          sdS[r * S::kPRow + c] = ds;
-        }
-      }
+    if (st0 < s1) ahead();
     __syncthreads();
-    add_product<D, RO>(acc0, kDq ? sP : sdS, sStr0, ty, tx);
-    if (!kDq) add_product<D, RO>(acc1, sP, sStr1, ty, tx);
+
+    float x[2][4], y[2][4];                          // own rows gid, gid + 8; streamed rows 8 h + 2 tig + {0, 1}
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) x[h][e] = y[h][e] = 0.0f;
+#pragma unroll 4
+    for (int ks = 0; ks < D / 16; ++ks) {
+      uint32_t a[3][4], b[3][4];
+#pragma unroll
+      for (int i = 0; i < 3; ++i) {
+        ldmatrix(a[i], a_row + i * S::kOwnPlane + ((ks * 32) ^ xor_first));
+        ldmatrix(b[i], b_row + i * S::kStrPlane + ((ks * 32) ^ xor_last));
+      }
+      mma_terms(x[0], x[1], a, b);
+#pragma unroll
+      for (int i = 0; i < 3; ++i) {
+        ldmatrix(a[i], a_row + (3 + i) * S::kOwnPlane + ((ks * 32) ^ xor_first));
+        ldmatrix(b[i], b_row + (3 + i) * S::kStrPlane + ((ks * 32) ^ xor_last));
+      }
+      mma_terms(y[0], y[1], a, b);
+    }
+    uint32_t wp[3][4], wd[3][4];                     // P and dS as operands
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      float pe[4], de[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int c = sg * 16 + 8 * h + 2 * tig + (e & 1);
+        const float l = kDq ? lse_own[e >> 1] : sLse[c], d = kDq ? delta_own[e >> 1] : sDelta[c];
+        pe[e] = c < n ? expf(fmaf(x[h][e], prm.scale, -l)) : 0.0f;
+        de[e] = c < n ? pe[e] * (y[h][e] - d) : 0.0f;
+      }
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        if (!kDq) split2(pe[2 * e], pe[2 * e + 1], wp[0][2 * h + e], wp[1][2 * h + e], wp[2][2 * h + e]);
+        split2(de[2 * e], de[2 * e + 1], wd[0][2 * h + e], wd[1][2 * h + e], wd[2][2 * h + e]);
+      }
+    }
+#pragma unroll
+    for (int c = 0; c < D / 16; ++c) {
+      uint32_t b[3][4];
+#pragma unroll
+      for (int i = 0; i < 3; ++i) ldmatrix_trans(b[i], w_row + i * S::kStrPlane + ((c * 32) ^ xor_first));
+      mma_terms(acc0[2 * c], acc0[2 * c + 1], wd, b);
+      if (!kDq) {
+#pragma unroll
+        for (int i = 0; i < 3; ++i) ldmatrix_trans(b[i], w_row + (3 + i) * S::kStrPlane + ((c * 32) ^ xor_first));
+        mma_terms(acc1[2 * c], acc1[2 * c + 1], wp, b);
+      }
+    }
   }
-  store_tile<D, RO>(static_cast<float*>(kDq ? prm.dq : prm.dk) + head * D, acc0, prm.scale, own0, own1, ty, tx);
-  if (!kDq) store_tile<D, RO>(static_cast<float*>(prm.dv) + head * D, acc1, 1.0f, own0, own1, ty, tx);
+
+  // Join of the groups of streamed rows, in order.
+  __syncthreads();
+  float4* join = reinterpret_cast<float4*>(smem + S::kStrAt);
+  auto slot = [&](int group, int x, int c) { return join + ((((group - 1) * 2 + x) * S::kRowGroups + rg) * (D / 8) + c) * 32 + lane; };
+  if (sg > 0) {
+#pragma unroll
+    for (int c = 0; c < D / 8; ++c) {
+      *slot(sg, 0, c) = make_float4(acc0[c][0], acc0[c][1], acc0[c][2], acc0[c][3]);
+      if (!kDq) *slot(sg, 1, c) = make_float4(acc1[c][0], acc1[c][1], acc1[c][2], acc1[c][3]);
+    }
+  }
+  __syncthreads();
+  if (sg > 0) return;
+  const int r = own0 + rg * 16 + gid;
+  auto finish = [&](float* dst, float (&acc)[D / 8][4], int x, float f) {
+#pragma unroll
+    for (int c = 0; c < D / 8; ++c) {
+#pragma unroll
+      for (int group = 1; group < S::kStrGroups; ++group) {
+        const float4 u = *slot(group, x, c);
+        acc[c][0] += u.x;
+        acc[c][1] += u.y;
+        acc[c][2] += u.z;
+        acc[c][3] += u.w;
+      }
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+        if (r + 8 * h < own1)
+          *reinterpret_cast<float2*>(dst + (head + r + 8 * h) * D + c * 8 + 2 * tig) = make_float2(acc[c][2 * h] * f, acc[c][2 * h + 1] * f);
+    }
+  };
+  finish(static_cast<float*>(kDq ? prm.dq : prm.dk), acc0, 0, prm.scale);
+  if (!kDq) finish(static_cast<float*>(prm.dv), acc1, 1, 1.0f);
 }
 
 // One launch for both: the heavier blocks (dK, dV: four products) first.
 template <int D, int kOwn>
-__global__ void __launch_bounds__(kThreads, D == 64 ? 2 : 1) attn_bwd_fma_kernel(const __grid_constant__ BwdParams prm) {
-  extern __shared__ __align__(16) float smem[];
+__global__ void __launch_bounds__(kThreads, D == 64 ? 2 : 1) attn_bwd_f32_kernel(const __grid_constant__ BwdParams prm) {
+  extern __shared__ __align__(16) uint8_t smem[];
   if (static_cast<int>(blockIdx.x) < prm.tiles_k)
-    fma_unit<D, kOwn, false>(prm, blockIdx.x, smem);
+    bwd_unit<D, kOwn, false>(prm, blockIdx.x, smem);
   else
-    fma_unit<D, kOwn, true>(prm, blockIdx.x - prm.tiles_k, smem);
+    bwd_unit<D, kOwn, true>(prm, blockIdx.x - prm.tiles_k, smem);
 }
 
 template <int D, int kOwn>
-int fma_impl(const BwdParams& prm, cudaStream_t st) {
-  constexpr int smem = Smem<D, kOwn>::kBytes;
-  cudaError_t e = cudaFuncSetAttribute(attn_bwd_fma_kernel<D, kOwn>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+int f32_impl(const BwdParams& prm, cudaStream_t st) {
+  constexpr int smem = Shape<D, kOwn>::kBytes;
+  cudaError_t e = cudaFuncSetAttribute(attn_bwd_f32_kernel<D, kOwn>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return static_cast<int>(e);
-  attn_bwd_fma_kernel<D, kOwn><<<dim3(prm.tiles_k + prm.tiles_q, prm.BH), kThreads, smem, st>>>(prm);
+  attn_bwd_f32_kernel<D, kOwn><<<dim3(prm.tiles_k + prm.tiles_q, prm.BH), kThreads, smem, st>>>(prm);
   return static_cast<int>(cudaGetLastError());
 }
 
@@ -306,9 +368,9 @@ int launch_delta(const void* o, const void* dout, const float* dlse, float* delt
                  : delta_impl<float, 128>(o, dout, dlse, delta, rows, st);
 }
 
-int launch_attn_bwd_fma(const BwdParams& prm, int own_rows, cudaStream_t st) {
-  if (own_rows == 64) return prm.D == 64 ? fma_impl<64, 64>(prm, st) : fma_impl<128, 64>(prm, st);
-  return prm.D == 64 ? fma_impl<64, 32>(prm, st) : fma_impl<128, 32>(prm, st);
+int launch_attn_bwd_f32(const BwdParams& prm, int own_rows, cudaStream_t st) {
+  if (own_rows == 64) return prm.D == 64 ? f32_impl<64, 64>(prm, st) : f32_impl<128, 64>(prm, st);
+  return prm.D == 64 ? f32_impl<64, 32>(prm, st) : f32_impl<128, 32>(prm, st);
 }
 
 }  // namespace pa

@@ -820,7 +820,7 @@ static int pa_attn_backward_impl(pa_ctx* ctx, const pa_attn_bwd_desc* d, void* s
     }
     e = pa::launch_delta(d->o, d->dout, d->dlse, d->delta, rows, d->D, d->dtype, st);
     if (e) return cuda_fail(ctx, e, "delta launch");
-    e = pa::launch_attn_bwd_fma(prm, own, st);
+    e = pa::launch_attn_bwd_f32(prm, own, st);
     return e ? cuda_fail(ctx, e, "attention backward launch") : PA_OK;
   }
   return d->P <= 32 ? launch_backward_tc<32>(ctx, d, tk, tq, st) : launch_backward_tc<PA_MAX_P>(ctx, d, tk, tq, st);

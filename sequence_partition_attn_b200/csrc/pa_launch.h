@@ -36,7 +36,7 @@ int launch_relayout(const void* src, void* dst, long long n0, long long n1, long
 // delta[row] = dout[row] . o[row] - dlse[row] (dlse may be null).
 int launch_delta(const void* o, const void* dout, const float* dlse, float* delta, long long rows, int D, int dtype,
                  cudaStream_t st);
-int launch_attn_bwd_fma(const BwdParams& prm, int own_rows, cudaStream_t st);     // own_rows 32 or 64
+int launch_attn_bwd_f32(const BwdParams& prm, int own_rows, cudaStream_t st);     // own_rows 32 or 64
 
 int attn_bwd_tc_tile_rows();
 int launch_attn_bwd_tc(const BwdTcParams<32>& prm, int D, cudaStream_t st);
