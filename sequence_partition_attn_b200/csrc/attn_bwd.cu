@@ -1,5 +1,5 @@
-// attn_bwd.cu -- backward pass of attention with reuse: the per-row terms and the kernels on
-// the FMA units (fp32 inputs).
+// attn_bwd.cu -- backward pass of attention with reuse: the per-row terms, and the gradients of
+// fp32 inputs (attn_bwd_tc.cu: bf16).
 //
 // With the merged outputs (O, LSE) of pa_partition_attn + pa_merge_states, the fresh pairs'
 // share of the output is P_ij v_j with P_ij = exp(s_ij - LSE_i), s = scale * q.k: the
@@ -9,10 +9,10 @@
 //   dQ_i = scale sum_j dS_ij k_j,    dK_j = scale sum_i dS_ij q_i,    dV_j = sum_i P_ij dO_i
 // over the fresh pairs.  P is recomputed from q, k and LSE, never stored.
 //
-// Two kernels, each owning the rows of what it sums and streaming the other side: one for
-// dQ (owns queries, streams keys), one for dK and dV (owns keys, streams queries).  Every sum
-// is taken by one block in a fixed order, so results do not change from run to run; the price
-// is that s and dO.v are computed twice (7 products instead of 5).
+// Blocks own the rows of what they sum and stream the other side: some for dQ (own queries,
+// stream keys), some for dK and dV (own keys, stream queries).  Every sum is taken by one block in
+// a fixed order, so results do not change from run to run; the price is that s and dO.v are
+// computed twice (7 products instead of 5).
 #include "pa_device.cuh"
 #include "pa_launch.h"
 
@@ -53,7 +53,10 @@ __global__ void __launch_bounds__(256) delta_kernel(const T* __restrict__ o, con
 // An fp32 value is a sum of three bf16 ones: x = x0 + x1 + x2 with x0 its upper half (cut, so that it
 // cannot overflow), x1 the rest rounded and x2 what is left, off by 2^-25 of x.  A product of two values takes
 // the six terms x0y0, x0y1, x1y0, x1y1, x0y2, x2y0; the others are below 2^-22 of it, and the sums
-// are fp32.  That is six bf16 products for one, at the tensor cores' rate.
+// are fp32.  That is six bf16 products for one, at the tensor cores' rate: 24 x 1536 x 128, all
+// pairs, takes 1.83 ms (56 fp32 TFLOP/s executed, 333 of bf16), and 2 x 1024 x 64 takes 57 us.  The
+// packed multiply-add units took 2.70 ms and 106 us.  Bound by the tensor cores' warp products,
+// then by the shared-memory reads of their operands (about 3/4 of the products' time).
 //
 // A block owns kOwn rows and streams tiles of the other side; its 8 warps are kOwn / 16 groups of
 // 16 own rows times kT / 16 groups of 16 streamed rows.  With A the own and B the streamed rows,
@@ -72,9 +75,12 @@ struct Shape {
   static constexpr int kOwnPlane = kOwn * kRow, kStrPlane = kT * kRow;
   static constexpr int kOwnAt = 0;                   // [tensor][plane][row][D] bf16
   static constexpr int kStrAt = kOwnAt + 6 * kOwnPlane;
-  static constexpr int kRawAt = kStrAt + 6 * kStrPlane;      // the next tile, [tensor][row][D] fp32
-  static constexpr int kStatAt = kRawAt + 2 * kT * D * 4;    // lse, delta by streamed row
-  static constexpr int kBytes = kStatAt + 2 * kT * 4;
+  static constexpr int kRawBytes = 2 * kT * D * 4, kStatBytes = 2 * kT * 4;
+  // two buffers of planes where they fit (all but D = 128 with 64 streamed rows)
+  static constexpr int kBuffers = kStrAt + 12 * kStrPlane + kRawBytes + 2 * kStatBytes <= 227 * 1024 ? 2 : 1;
+  static constexpr int kRawAt = kStrAt + kBuffers * 6 * kStrPlane;      // the tile after, [tensor][row][D] fp32
+  static constexpr int kStatAt = kRawAt + kRawBytes;         // lse, delta by streamed row, per buffer
+  static constexpr int kBytes = kStatAt + kBuffers * kStatBytes;
   static_assert((kStrGroups - 1) * 2 * kOwn * D * 4 <= kStatAt - kStrAt, "the join reuses the streamed tiles");
 };
 
@@ -91,13 +97,32 @@ __device__ __forceinline__ void mma(float (&c)[4], const uint32_t (&a)[4], uint3
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
-// c0 += a b for columns 0..7 of b, c1 for columns 8..15; all six terms, the smallest first.
-__device__ __forceinline__ void mma_terms(float (&c0)[4], float (&c1)[4], const uint32_t (&a)[3][4], const uint32_t (&b)[3][4]) {
+// c0 += a b for columns 0..7 of b, c1 for columns 8..15, and the same for d, x and y: all six terms,
+// the smallest first, on four sums in turn (a product takes as long as four take to issue).  The
+// tensor cores cut their sums instead of rounding them, which adds up over a long axis (an error of
+// 5e-6 of the gradients of 1024 rows; plain fp32 sums 7e-7, these 4e-7): the terms of each 16 summed elements start
+// from zero and are added to the running sums in fp32.
+__device__ __forceinline__ void mma_terms(float (&c0)[4], float (&c1)[4], const uint32_t (&a)[3][4], const uint32_t (&b)[3][4],
+                                          float (&d0)[4], float (&d1)[4], const uint32_t (&x)[3][4], const uint32_t (&y)[3][4]) {
   constexpr int ia[6] = {0, 2, 1, 0, 1, 0}, ib[6] = {2, 0, 1, 1, 0, 0};
+  float s[4][4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) s[i][e] = 0.0f;
 #pragma unroll
   for (int i = 0; i < 6; ++i) {
-    mma(c0, a[ia[i]], b[ib[i]][0], b[ib[i]][1]);
-    mma(c1, a[ia[i]], b[ib[i]][2], b[ib[i]][3]);
+    mma(s[0], a[ia[i]], b[ib[i]][0], b[ib[i]][1]);
+    mma(s[1], a[ia[i]], b[ib[i]][2], b[ib[i]][3]);
+    mma(s[2], x[ia[i]], y[ib[i]][0], y[ib[i]][1]);
+    mma(s[3], x[ia[i]], y[ib[i]][2], y[ib[i]][3]);
+  }
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    c0[e] += s[0][e];
+    c1[e] += s[1][e];
+    d0[e] += s[2][e];
+    d1[e] += s[3][e];
   }
 }
 
@@ -134,8 +159,7 @@ __device__ __forceinline__ void bwd_unit(const BwdParams& prm, int tile, uint8_t
   const int rg = warp % S::kRowGroups, sg = warp / S::kRowGroups;
   const int gid = lane >> 2, tig = lane & 3;
   const uint32_t sbase = smem_u32(smem);
-  float* sLse = reinterpret_cast<float*>(smem + S::kStatAt);
-  float* sDelta = sLse + kT;
+  float* stats = reinterpret_cast<float*>(smem + S::kStatAt);
   int g = 0;
   while (g + 1 < t.QG && t.tile_start[g + 1] <= tile) ++g;
   const int own0 = t.qg_row0[g] + (tile - t.tile_start[g]) * kOwn;
@@ -203,45 +227,60 @@ __device__ __forceinline__ void bwd_unit(const BwdParams& prm, int tile, uint8_t
   const uint32_t rows_first = (swz + ((lane >> 3) & 1) * 8) * S::kRow, rows_last = (swz + (lane >> 4) * 8) * S::kRow;
   const uint32_t xor_first = ((lane >> 4) ^ swz) << 4, xor_last = (((lane >> 3) & 1) ^ swz) << 4;
   const uint32_t a_row = sbase + S::kOwnAt + rg * 16 * S::kRow + rows_first;
-  const uint32_t b_row = sbase + S::kStrAt + sg * 16 * S::kRow + rows_last;
-  const uint32_t w_row = sbase + S::kStrAt + sg * 16 * S::kRow + rows_first;
+  const uint32_t b_row0 = sbase + S::kStrAt + sg * 16 * S::kRow + rows_last;
+  const uint32_t w_row0 = sbase + S::kStrAt + sg * 16 * S::kRow + rows_first;
 
+  // Tile i is used while tile i + 1 is split and tile i + 2 copied.  With two buffers, half of the
+  // warps (one of each scheduler's two) split first and the others last, so that one splits while
+  // the other feeds the tensor cores.
   int s0, s1;
   int p = next_range(t, g, 0, s0, s1);
   int st0 = s0;
-  float lse_next = INFINITY, delta_next = 0.0f;      // of streamed row threadIdx.x of the next tile
-  auto ahead = [&]() {
+  int copied = 0, ready = 0;                         // rows of the copied and of the split tile
+  float lse_next = INFINITY, delta_next = 0.0f;      // of row threadIdx.x of the copied tile
+  auto copy = [&]() {
+    copied = 0;
+    if (st0 >= s1) return;
+    copied = min(kT, s1 - st0);
     fetch(st0, s1);
     if (!kDq && threadIdx.x < kT) {
       const int r = st0 + threadIdx.x;
       lse_next = stat_lse(r, s1);
       delta_next = r < s1 ? prm.delta[head + r] : 0.0f;
     }
+    st0 += kT;
+    if (st0 >= s1) {
+      p = next_range(t, g, p, s0, s1);
+      st0 = s0;
+    }
   };
-  if (st0 < s1) ahead();
-  while (st0 < s1) {
+  auto split = [&](int buf) {
+    ready = copied;
+    if (copied == 0) return;
     asm volatile("cp.async.wait_all;" ::: "memory");
-    __syncthreads();                                 // the tile before is used up
 #pragma unroll
     for (int x = 0; x < 2; ++x)
 #pragma unroll
       for (int n = 0; n < kPieces; ++n) {
         const int i = n * kThreads + threadIdx.x;
         const float4* raw = reinterpret_cast<const float4*>(smem + S::kRawAt + (x * kT * D + i * 8) * 4);
-        split_store<S::kStrPlane>(smem + S::kStrAt + x * 3 * S::kStrPlane, S::kRow, i / (D / 8), i % (D / 8), raw[0], raw[1]);
+        split_store<S::kStrPlane>(smem + S::kStrAt + (buf * 6 + x * 3) * S::kStrPlane, S::kRow, i / (D / 8), i % (D / 8), raw[0], raw[1]);
       }
     if (!kDq && threadIdx.x < kT) {
-      sLse[threadIdx.x] = lse_next;
-      sDelta[threadIdx.x] = delta_next;
+      stats[buf * 2 * kT + threadIdx.x] = lse_next;
+      stats[buf * 2 * kT + kT + threadIdx.x] = delta_next;
     }
-    const int n = min(kT, s1 - st0);
-    st0 += kT;
-    if (st0 >= s1) {
-      p = next_range(t, g, p, s0, s1);
-      st0 = s0;
-    }
-    if (st0 < s1) ahead();
-    __syncthreads();
+    copy();
+  };
+  copy();
+  split(0);
+  __syncthreads();
+  for (int buf = 0; ready > 0;) {
+    const int n = ready, next = S::kBuffers == 2 ? buf ^ 1 : 0;
+    const float* sLse = stats + buf * 2 * kT;
+    const float* sDelta = sLse + kT;
+    const uint32_t b_row = b_row0 + buf * 6 * S::kStrPlane, w_row = w_row0 + buf * 6 * S::kStrPlane;
+    if (S::kBuffers == 2 && warp < 4) split(next);
 
     float x[2][4], y[2][4];                          // own rows gid, gid + 8; streamed rows 8 h + 2 tig + {0, 1}
 #pragma unroll
@@ -250,19 +289,15 @@ __device__ __forceinline__ void bwd_unit(const BwdParams& prm, int tile, uint8_t
       for (int e = 0; e < 4; ++e) x[h][e] = y[h][e] = 0.0f;
 #pragma unroll 4
     for (int ks = 0; ks < D / 16; ++ks) {
-      uint32_t a[3][4], b[3][4];
+      uint32_t a0[3][4], b0[3][4], a1[3][4], b1[3][4];
 #pragma unroll
       for (int i = 0; i < 3; ++i) {
-        ldmatrix(a[i], a_row + i * S::kOwnPlane + ((ks * 32) ^ xor_first));
-        ldmatrix(b[i], b_row + i * S::kStrPlane + ((ks * 32) ^ xor_last));
+        ldmatrix(a0[i], a_row + i * S::kOwnPlane + ((ks * 32) ^ xor_first));
+        ldmatrix(b0[i], b_row + i * S::kStrPlane + ((ks * 32) ^ xor_last));
+        ldmatrix(a1[i], a_row + (3 + i) * S::kOwnPlane + ((ks * 32) ^ xor_first));
+        ldmatrix(b1[i], b_row + (3 + i) * S::kStrPlane + ((ks * 32) ^ xor_last));
       }
-      mma_terms(x[0], x[1], a, b);
-#pragma unroll
-      for (int i = 0; i < 3; ++i) {
-        ldmatrix(a[i], a_row + (3 + i) * S::kOwnPlane + ((ks * 32) ^ xor_first));
-        ldmatrix(b[i], b_row + (3 + i) * S::kStrPlane + ((ks * 32) ^ xor_last));
-      }
-      mma_terms(y[0], y[1], a, b);
+      mma_terms(x[0], x[1], a0, b0, y[0], y[1], a1, b1);
     }
     uint32_t wp[3][4], wd[3][4];                     // P and dS as operands
 #pragma unroll
@@ -281,22 +316,27 @@ __device__ __forceinline__ void bwd_unit(const BwdParams& prm, int tile, uint8_t
         split2(de[2 * e], de[2 * e + 1], wd[0][2 * h + e], wd[1][2 * h + e], wd[2][2 * h + e]);
       }
     }
+    // 16 channels of dK and dV at a time, 32 of dQ
 #pragma unroll
-    for (int c = 0; c < D / 16; ++c) {
-      uint32_t b[3][4];
+    for (int c = 0; c < D / 16; c += kDq ? 2 : 1) {
+      uint32_t b0[3][4], b1[3][4];
 #pragma unroll
-      for (int i = 0; i < 3; ++i) ldmatrix_trans(b[i], w_row + i * S::kStrPlane + ((c * 32) ^ xor_first));
-      mma_terms(acc0[2 * c], acc0[2 * c + 1], wd, b);
-      if (!kDq) {
-#pragma unroll
-        for (int i = 0; i < 3; ++i) ldmatrix_trans(b[i], w_row + (3 + i) * S::kStrPlane + ((c * 32) ^ xor_first));
-        mma_terms(acc1[2 * c], acc1[2 * c + 1], wp, b);
+      for (int i = 0; i < 3; ++i) {
+        ldmatrix_trans(b0[i], w_row + i * S::kStrPlane + ((c * 32) ^ xor_first));
+        ldmatrix_trans(b1[i], w_row + (kDq ? i : 3 + i) * S::kStrPlane + (((kDq ? c + 1 : c) * 32) ^ xor_first));
       }
+      if (kDq)
+        mma_terms(acc0[2 * c], acc0[2 * c + 1], wd, b0, acc0[(2 * c + 2) % (D / 8)], acc0[(2 * c + 3) % (D / 8)], wd, b1);
+      else
+        mma_terms(acc0[2 * c], acc0[2 * c + 1], wd, b0, acc1[2 * c], acc1[2 * c + 1], wp, b1);
     }
+    if (S::kBuffers == 1) __syncthreads();
+    if (S::kBuffers == 1 || warp >= 4) split(next);
+    __syncthreads();
+    buf = next;
   }
 
   // Join of the groups of streamed rows, in order.
-  __syncthreads();
   float4* join = reinterpret_cast<float4*>(smem + S::kStrAt);
   auto slot = [&](int group, int x, int c) { return join + ((((group - 1) * 2 + x) * S::kRowGroups + rg) * (D / 8) + c) * 32 + lane; };
   if (sg > 0) {
@@ -332,7 +372,7 @@ __device__ __forceinline__ void bwd_unit(const BwdParams& prm, int tile, uint8_t
 
 // One launch for both: the heavier blocks (dK, dV: four products) first.
 template <int D, int kOwn>
-__global__ void __launch_bounds__(kThreads, D == 64 ? 2 : 1) attn_bwd_f32_kernel(const __grid_constant__ BwdParams prm) {
+__global__ void __launch_bounds__(kThreads, D == 64 && kOwn == 64 ? 2 : 1) attn_bwd_f32_kernel(const __grid_constant__ BwdParams prm) {
   extern __shared__ __align__(16) uint8_t smem[];
   if (static_cast<int>(blockIdx.x) < prm.tiles_k)
     bwd_unit<D, kOwn, false>(prm, blockIdx.x, smem);

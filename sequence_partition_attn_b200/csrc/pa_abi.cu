@@ -810,11 +810,15 @@ static int pa_attn_backward_impl(pa_ctx* ctx, const pa_attn_bwd_desc* d, void* s
     prm.N = d->N;
     prm.D = d->D;
     prm.scale = d->scale;
-    int own = 64;
+    // Blocks of 32 rows halve the time of one block and stream the other side twice as often: they
+    // are taken when all of them run at once.  us on a B200, 32 against 64 rows: 2 x 1024 x 64 (128
+    // blocks of 32 rows) 61 / 110, 4 x 1024 x 64 (256) 112 / 113, 2 x 1024 x 128 115 / 172,
+    // 4 x 1024 x 128 221 / 173.
+    int own = 32;
     prm.tiles_q = fill_owner_tiles(prm.tq, own);
     prm.tiles_k = fill_owner_tiles(prm.tk, own);
-    if (BH * (prm.tiles_q + prm.tiles_k) < 2 * ctx->sm_count) {
-      own = 32;
+    if (BH * (prm.tiles_q + prm.tiles_k) > ctx->sm_count) {
+      own = 64;
       prm.tiles_q = fill_owner_tiles(prm.tq, own);
       prm.tiles_k = fill_owner_tiles(prm.tk, own);
     }
