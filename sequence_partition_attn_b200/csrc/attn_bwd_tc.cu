@@ -180,7 +180,7 @@ __device__ __forceinline__ void dkdv_unit(const BwdTcParams<MP>& prm, int unit, 
           w.next();
         };
         bool ok = wait(L::KV_FULL, 0) && wait(L::Q_FULL, 0) && wait(L::O_FULL, 0);
-        int done = 0;                    // tiles whose Q_EMPTY, O_EMPTY commits were issued
+        int done = 0, freed = 0;         // Q_EMPTY, O_EMPTY commits issued
         if (ok) {
           if (shorts) fix(0, 0);
           tc_fence_after();
@@ -208,6 +208,7 @@ __device__ __forceinline__ void dkdv_unit(const BwdTcParams<MP>& prm, int unit, 
           tc_fence_after();
           product_w<D, 64, 0xCC>(tDV, tX, mnmajor(sO(u)), false);
           commit(L::O_EMPTY + u);
+          ++freed;
           if (more) {
             product_nt<D>(tX, aK, kmajor(sQ(s1)));
             commit(L::S_FULL);
@@ -227,7 +228,7 @@ __device__ __forceinline__ void dkdv_unit(const BwdTcParams<MP>& prm, int unit, 
           u = u1;
         }
         {                                // the last commits arrive before the CTA exits
-          for (int i = max(0, done - kOStages); i < done; ++i) mbar_drain(bar(L::O_EMPTY + i % kOStages), (i / kOStages) & 1);
+          for (int i = max(0, freed - kOStages); i < freed; ++i) mbar_drain(bar(L::O_EMPTY + i % kOStages), (i / kOStages) & 1);
           for (int i = max(0, done - kQStages); i < done; ++i) mbar_drain(bar(L::Q_EMPTY + i % kQStages), (i / kQStages) & 1);
         }
       }
@@ -436,7 +437,7 @@ __device__ __forceinline__ void dq_unit(const BwdTcParams<MP>& prm, int unit, ui
           w.next();
         };
         bool ok = wait(L::OWN_FULL, 0) && wait(L::K_FULL, 0) && wait(L::V_FULL, 0) && (n_tiles < 2 || wait(L::K_FULL + 1, 0));
-        int done = 0;
+        int done = 0, freed = 0;         // K_EMPTY, V_EMPTY commits issued
         if (ok) {
           if (shorts) {
             fix(wk, L::kK);
@@ -448,6 +449,7 @@ __device__ __forceinline__ void dq_unit(const BwdTcParams<MP>& prm, int unit, ui
           commit(L::S_FULL);
           product_nt<D>(region(1), aO, kmajor(sV(0)));
           commit(L::V_EMPTY);
+          ++freed;
           commit(L::DP_FULL);
           if (n_tiles > 1) {
             product_nt<D>(region(2), aQ, kmajor(sK(1)));
@@ -469,6 +471,7 @@ __device__ __forceinline__ void dq_unit(const BwdTcParams<MP>& prm, int unit, ui
             tc_fence_after();
             product_nt<D>(tS, aO, kmajor(base + L::kV + (b ^ 1) * L::kTile));       // dP(j + 1) over S(j)
             commit(L::V_EMPTY + (b ^ 1));
+            ++freed;
             commit(L::DP_FULL + (b ^ 1));
           }
           if (!(ok = wait(L::DS_FULL + b, ph))) break;
@@ -488,8 +491,8 @@ __device__ __forceinline__ void dq_unit(const BwdTcParams<MP>& prm, int unit, ui
           s = s == kKStages - 1 ? 0 : s + 1;
           r = r == 0 ? 2 : r - 1;                             // 2 (j + 1) % 3
         }
-        for (int i = max(0, done - kKStages); i < done; ++i)
-            mbar_drain(bar(L::K_EMPTY + i % kKStages), (i / kKStages) & 1);
+        for (int i = max(0, done - kKStages); i < done; ++i) mbar_drain(bar(L::K_EMPTY + i % kKStages), (i / kKStages) & 1);
+        for (int i = max(0, freed - kVStages); i < freed; ++i) mbar_drain(bar(L::V_EMPTY + i % kVStages), (i / kVStages) & 1);
       }
     }
   } else {
