@@ -9,7 +9,7 @@
 // products read.  The scale is a power of two, so code * scale is exact in bf16: nothing is
 // rounded that the cache did not round already, and the scores need no scale of their own.
 // The codes cross HBM and L2 in 8 bits; a pass that widened the cache to bf16 first would write
-// and read it again at twice the size.  24 heads x 9450 queries x 18900 tokens, D = 128: 1.56 ms, a
+// and read it again at twice the size.  40 heads x 9450 queries x 9450 tokens, D = 128: 1.6 ms, a
 // tile of 128 tokens every 3800 cycles, of which the softmax warps work 2200 and wait for the
 // products between.  (Loads into registers one block ahead: 1.93 ms, as L2 answers in about a
 // thousand cycles and a tile has four of them in a row.  f16 tiles with the scales in the softmax
@@ -17,8 +17,9 @@
 //
 // Roles (512 threads, one CTA per SM; 128 registers at launch, then 80 / 176 / 176 / 80):
 //   warp 0      loads Q_a, Q_b by TMA.     warp 1  TMEM owner and MMA issuer.
-//   warps 4..7  softmax of query tile a; warps 8..11 of tile b (one row per thread).
-//   warps 12..15 widen K and V; after the last tile they store O and LSE.
+//   warps 4..7  softmax of query tile a; warps 8..11 of tile b (one row per thread), and at the end
+//               the stores of its O and LSE.
+//   warps 12..15 widen K and V.
 // Rows are the (H / Hk) * Nq queries of one KV head.  A block of at most 128 rows runs tile a only.
 #include <cuda_fp16.h>
 
@@ -50,7 +51,7 @@ struct Layout {
   static constexpr int kBar = kCodes + 4 * kItem;
   enum { Q_FULL = 0, K_FULL = 1, V_FULL = K_FULL + kStages, K_EMPTY = V_FULL + kStages,
          V_EMPTY = K_EMPTY + kStages, S_FULL = V_EMPTY + kStages, P_LO = S_FULL + 2, P_HI = P_LO + 2,
-         O_FINAL = P_HI + 2, ML_FULL = O_FINAL + 2, NBAR = ML_FULL + 2 };
+         O_FINAL = P_HI + 2, NBAR = O_FINAL + 2 };
   static constexpr int kSlot = kBar + NBAR * 8;
   static constexpr int kAbort = kSlot + 8;
   static constexpr int kBytes = kAbort + 8 + 1024;
@@ -170,7 +171,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attn_tc_kernel(const __grid
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < L::NBAR; ++i) {
-      const bool threads = (i >= L::K_FULL && i < L::K_EMPTY) || (i >= L::P_LO && i < L::O_FINAL) || i >= L::ML_FULL;
+      const bool threads = (i >= L::K_FULL && i < L::K_EMPTY) || (i >= L::P_LO && i < L::O_FINAL);
       mbar_init(bar(i), threads ? 128u : 1u);
     }
     *abort_flag = 0;
@@ -308,14 +309,40 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attn_tc_kernel(const __grid
       }
       const float2 a = __fadd2_rn(__fadd2_rn(acc[0], acc[1]), __fadd2_rn(acc[2], acc[3]));
       l += a.x + a.y;
-      if (j == T - 1) {
-        // over Q_x, whose last product is done
-        reinterpret_cast<float2*>(gbase + L::kQ + x * L::kTile)[row] = make_float2(m, l);
-        mbar_arrive(bar(L::ML_FULL + x));
+    }
+    const int r = row0 + x * kBM + row;
+    if (x < nx && (T == 0 || mbar_wait(bar(L::O_FINAL + x), 0, abort_flag, status))) {
+      tc_fence_after();
+      const bool row_ok = r < prm.R;
+      const size_t at = (prm.splits > 1 ? static_cast<size_t>(split) * prm.rows : 0) + static_cast<size_t>(bh) * prm.R + r;
+      const float inv = 1.0f / l;
+#pragma unroll 2
+      for (int c = 0; c < D / 16; ++c) {
+        float v[16];
+        if (T > 0) {
+          uint32_t u[16];
+          tmem_ld16(tO + c * 16, u);
+          tmem_wait_ld();
+#pragma unroll
+          for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(u[i]) * inv;
+        } else {
+#pragma unroll
+          for (int i = 0; i < 16; ++i) v[i] = 0.0f;
+        }
+        if (!row_ok) continue;
+        if (prm.splits > 1) {
+#pragma unroll
+          for (int i = 0; i < 16; i += 4) store4(prm.ws_o + at * D + c * 16 + i, make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]));
+        } else {
+          uint4* o = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(prm.o) + at * D + c * 16);
+          o[0] = make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]));
+          o[1] = make_uint4(pack_bf16x2(v[8], v[9]), pack_bf16x2(v[10], v[11]), pack_bf16x2(v[12], v[13]), pack_bf16x2(v[14], v[15]));
+        }
       }
+      if (row_ok) (prm.splits > 1 ? prm.ws_lse : prm.lse)[at] = T > 0 ? (m + fast_log2(l)) * kLn2 : -INFINITY;
     }
   } else {
-    // ---------------------------------------------------------------- widening, then the stores
+    // ---------------------------------------------------------------- widening
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsWiden));
     const int thread = threadIdx.x - 384;
     const size_t head = static_cast<size_t>(bh) * prm.M * D;
@@ -359,45 +386,6 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attn_tc_kernel(const __grid
       }
     }
     asm volatile("cp.async.wait_all;" ::: "memory");
-    const int row = (warp & 3) * 32 + lane;
-    const uint32_t lane_off = static_cast<uint32_t>((warp & 3) * 32) << 16;
-    for (int x = 0; ok && x < nx; ++x) {
-      const int r = row0 + x * kBM + row;
-      const bool row_ok = r < prm.R;
-      const size_t at = (prm.splits > 1 ? static_cast<size_t>(split) * prm.rows : 0) + static_cast<size_t>(bh) * prm.R + r;
-      float2 ml = make_float2(-INFINITY, 1.0f);
-      if (T > 0) {
-        if (!mbar_wait(bar(L::O_FINAL + x), 0, abort_flag, status) ||
-            !mbar_wait(bar(L::ML_FULL + x), 0, abort_flag, status))
-          break;
-        tc_fence_after();
-        ml = reinterpret_cast<const float2*>(gbase + L::kQ + x * L::kTile)[row];
-      }
-      const float inv = 1.0f / ml.y;
-#pragma unroll 1
-      for (int c = 0; c < D / 16; ++c) {
-        uint32_t v[16];
-        if (T > 0) {
-          tmem_ld16(tmem + lane_off + 256 + x * 128 + c * 16, v);
-          tmem_wait_ld();
-        } else {
-#pragma unroll
-          for (int i = 0; i < 16; ++i) v[i] = 0u;
-        }
-        if (row_ok) {
-#pragma unroll
-          for (int i = 0; i < 16; i += 4) {
-            const float4 o = make_float4(__uint_as_float(v[i]) * inv, __uint_as_float(v[i + 1]) * inv,
-                                         __uint_as_float(v[i + 2]) * inv, __uint_as_float(v[i + 3]) * inv);
-            if (prm.splits > 1)
-              store4(prm.ws_o + at * D + c * 16 + i, o);
-            else
-              store4(static_cast<__nv_bfloat16*>(prm.o) + at * D + c * 16 + i, o);
-          }
-        }
-      }
-      if (row_ok) (prm.splits > 1 ? prm.ws_lse : prm.lse)[at] = T > 0 ? (ml.x + fast_log2(ml.y)) * kLn2 : -INFINITY;
-    }
   }
 
   tc_fence_before();
