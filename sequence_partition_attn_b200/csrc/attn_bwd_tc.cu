@@ -14,8 +14,10 @@
 // neither goes through shared memory.
 //
 // Roles (384 threads, one CTA per SM).  warp 0: TMA producer.  warp 1: TMEM owner and MMA issuer
-// (whole warp, one elected lane issues; it also zeroes the rows behind a range shorter than a
-// tile).  warp 3 (dK, dV): -LSE and -delta of the streamed queries into shared memory.  warps
+// (one thread).  warp 2, where a group streams a range shorter than a tile: zeroes the rows behind
+// it, which may hold anything, and passes every tile on to the issuer (22 x 10 tokens in 32
+// partitions: 28 us; 360 us with the issuing thread zeroing).  warp 3 (dK, dV): -LSE and -delta of
+// the streamed queries into shared memory.  warps
 // 4-7 and 8-11: two warpgroups, one TMEM lane per thread, columns 0-63 and 64-127 of the scores.
 // Launched at 168 registers: warpgroup 0 drops to 88, the others rise to 208.
 //
@@ -47,16 +49,6 @@ __device__ __forceinline__ void read_scores(uint32_t tmem, float (&s)[64]) {
   tmem_wait_ld();
 #pragma unroll
   for (int i = 0; i < 64; ++i) s[i] = __uint_as_float(r[i]);
-}
-
-template <int MP>
-__device__ __forceinline__ bool has_short_range(const BwdSide<MP>& t, int g) {
-  for (int p = 0; p < t.P;) {
-    int s0, s1;
-    p = next_range(t, g, p, s0, s1);
-    if (s1 > s0 && s1 - s0 < kRows) return true;
-  }
-  return false;
 }
 
 // The group, head and first row of a unit: groups in launch order, heads and then tiles in each.
@@ -96,7 +88,8 @@ struct KvLayout {
   static constexpr int kBar = kStat + 2 * 2 * kRows * 4;
   enum { KV_FULL = 0, Q_FULL = 1, O_FULL = Q_FULL + kQStages, Q_EMPTY = O_FULL + kOStages,
          O_EMPTY = Q_EMPTY + kQStages, STAT_FULL = O_EMPTY + kOStages, STAT_EMPTY = STAT_FULL + 2,
-         S_FULL = STAT_EMPTY + 2, DP_FULL, P_LO, P_HI, DS_FULL, FINAL, NBAR };
+         S_FULL = STAT_EMPTY + 2, DP_FULL, P_LO, P_HI, DS_FULL, FINAL,
+         Q_FIXED, O_FIXED = Q_FIXED + kQStages, NBAR = O_FIXED + kOStages };
   static constexpr int kSlot = kBar + NBAR * 8;
   static constexpr int kAbort = kSlot + 8;
   static constexpr int kBytes = kAbort + 8;
@@ -118,7 +111,7 @@ __device__ __forceinline__ void dkdv_unit(const BwdTcParams<MP>& prm, int unit, 
   if (threadIdx.x == 0) {
     for (int i = 0; i < L::NBAR; ++i) {
       uint32_t n = 1;
-      if (i == L::STAT_FULL || i == L::STAT_FULL + 1) n = 32;
+      if (i == L::STAT_FULL || i == L::STAT_FULL + 1 || i >= L::Q_FIXED) n = 32;
       if (i == L::STAT_EMPTY || i == L::STAT_EMPTY + 1 || i == L::P_LO || i == L::P_HI || i == L::DS_FULL) n = 256;
       mbar_init(bar(i), n);
     }
@@ -136,7 +129,8 @@ __device__ __forceinline__ void dkdv_unit(const BwdTcParams<MP>& prm, int unit, 
   const uint32_t tX = tmem, tY = tmem + 128, tDV = tmem + 256, tDK = tmem + 384;
   auto sQ = [&](int s) { return base + L::kQ + s * L::kTile; };
   auto sO = [&](int u) { return base + L::kO + u * L::kTile; };
-  const int n_tiles = count_tiles(t, g);
+  const int n_tiles = t.tiles[g];
+  const bool shorts = t.shorts[g];
 
   if (warp < 4) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsLow));
@@ -169,20 +163,10 @@ __device__ __forceinline__ void dkdv_unit(const BwdTcParams<MP>& prm, int unit, 
         const uint64_t aK = kmajor(base + L::kK), aV = kmajor(base + L::kV);
         auto wait = [&](int b, uint32_t parity) { return mbar_wait(bar(b), parity & 1, abort_flag, status); };
         auto commit = [&](int b) { mma_commit(bar(b)); };
-        TileWalk w(t, g);
-        const bool shorts = has_short_range(t, g);
-        // Tile j's operands arrived: zero behind a short range.
-        auto fix = [&](int s, int u) {
-          if (w.is_short()) {
-            zero_rows<D>(gbase + L::kQ + s * L::kTile, w.last());
-            zero_rows<D>(gbase + L::kO + u * L::kTile, w.last());
-          }
-          w.next();
-        };
-        bool ok = wait(L::KV_FULL, 0) && wait(L::Q_FULL, 0) && wait(L::O_FULL, 0);
+        const int q_full = shorts ? L::Q_FIXED : L::Q_FULL, o_full = shorts ? L::O_FIXED : L::O_FULL;
+        bool ok = wait(L::KV_FULL, 0) && wait(q_full, 0) && wait(o_full, 0);
         int done = 0, freed = 0;         // Q_EMPTY, O_EMPTY commits issued
         if (ok) {
-          if (shorts) fix(0, 0);
           tc_fence_after();
           product_nt<D>(tX, aK, kmajor(sQ(0)));
           commit(L::S_FULL);
@@ -196,8 +180,7 @@ __device__ __forceinline__ void dkdv_unit(const BwdTcParams<MP>& prm, int unit, 
           const bool more = j + 1 < n_tiles;
           if (s1 == 0) phq ^= 1;
           if (more) {
-            ok = wait(L::Q_FULL + s1, phq) && wait(L::O_FULL + u1, (j + 1) / kOStages) && wait(L::P_LO, j);
-            if (ok && shorts) fix(s1, u1);
+            ok = wait(q_full + s1, phq) && wait(o_full + u1, (j + 1) / kOStages) && wait(L::P_LO, j);
           } else {
             ok = wait(L::P_LO, j);
           }
@@ -231,6 +214,18 @@ __device__ __forceinline__ void dkdv_unit(const BwdTcParams<MP>& prm, int unit, 
           for (int i = max(0, freed - kOStages); i < freed; ++i) mbar_drain(bar(L::O_EMPTY + i % kOStages), (i / kOStages) & 1);
           for (int i = max(0, done - kQStages); i < done; ++i) mbar_drain(bar(L::Q_EMPTY + i % kQStages), (i / kQStages) & 1);
         }
+      }
+    } else if (warp == 2 && shorts) {
+      // ---------------------------------------------------------------- rows behind short ranges
+      int j = 0;
+      for (TileWalk w(t, g); w.valid(); w.next(), ++j) {
+        const int s = j % kQStages, u = j % kOStages;
+        if (!mbar_wait_warp(bar(L::Q_FULL + s), (j / kQStages) & 1, abort_flag, status)) break;
+        if (w.is_short()) zero_rows<D>(gbase + L::kQ + s * L::kTile, w.last(), lane);
+        mbar_arrive(bar(L::Q_FIXED + s));
+        if (!mbar_wait_warp(bar(L::O_FULL + u), (j / kOStages) & 1, abort_flag, status)) break;
+        if (w.is_short()) zero_rows<D>(gbase + L::kO + u * L::kTile, w.last(), lane);
+        mbar_arrive(bar(L::O_FIXED + u));
       }
     } else if (warp == 3) {
       // ---------------------------------------------------------------- LSE and delta
@@ -360,7 +355,8 @@ struct QLayout {
   static constexpr int kBar = kV + kVStages * kTile;
   enum { OWN_FULL = 0, K_FULL = 1, V_FULL = K_FULL + kKStages, K_EMPTY = V_FULL + kVStages,
          V_EMPTY = K_EMPTY + kKStages, S_FULL = V_EMPTY + kVStages,
-         DP_FULL = S_FULL + 2, S_READ = DP_FULL + 2, DS_FULL = S_READ + 2, FINAL = DS_FULL + 2, NBAR };
+         DP_FULL = S_FULL + 2, S_READ = DP_FULL + 2, DS_FULL = S_READ + 2, FINAL = DS_FULL + 2,
+         K_FIXED, V_FIXED = K_FIXED + kKStages, NBAR = V_FIXED + kVStages };
   static constexpr int kSlot = kBar + NBAR * 8;
   static constexpr int kAbort = kSlot + 8;
   static constexpr int kBytes = kAbort + 8;
@@ -381,7 +377,7 @@ __device__ __forceinline__ void dq_unit(const BwdTcParams<MP>& prm, int unit, ui
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < L::NBAR; ++i)
-      mbar_init(bar(i), i >= L::S_READ && i < L::FINAL ? 256u : 1u);
+      mbar_init(bar(i), i >= L::S_READ && i < L::FINAL ? 256u : i >= L::K_FIXED ? 32u : 1u);
     *abort_flag = 0;
     fence_mbar_init();
   }
@@ -397,7 +393,8 @@ __device__ __forceinline__ void dq_unit(const BwdTcParams<MP>& prm, int unit, ui
   auto region = [&](int i) { return tmem + 128u * (i % 3); };
   auto sK = [&](int j) { return base + L::kK + (j % kKStages) * L::kTile; };
   auto sV = [&](int j) { return base + L::kV + (j % kVStages) * L::kTile; };
-  const int n_tiles = count_tiles(t, g);
+  const int n_tiles = t.tiles[g];
+  const bool shorts = t.shorts[g];
 
   if (warp < 4) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsLow));
@@ -429,21 +426,10 @@ __device__ __forceinline__ void dq_unit(const BwdTcParams<MP>& prm, int unit, ui
         const uint64_t aQ = kmajor(base + L::kQ), aO = kmajor(base + L::kO);
         auto wait = [&](int b, uint32_t parity) { return mbar_wait(bar(b), parity & 1, abort_flag, status); };
         auto commit = [&](int b) { mma_commit(bar(b)); };
-        TileWalk wk(t, g), wv(t, g);
-        const bool shorts = has_short_range(t, g);
-        // A tile arrived: zero behind a short range.
-        auto fix = [&](auto& w, int at) {
-          if (w.is_short()) zero_rows<D>(gbase + at, w.last());
-          w.next();
-        };
-        bool ok = wait(L::OWN_FULL, 0) && wait(L::K_FULL, 0) && wait(L::V_FULL, 0) && (n_tiles < 2 || wait(L::K_FULL + 1, 0));
+        const int k_full = shorts ? L::K_FIXED : L::K_FULL, v_full = shorts ? L::V_FIXED : L::V_FULL;
+        bool ok = wait(L::OWN_FULL, 0) && wait(k_full, 0) && wait(v_full, 0) && (n_tiles < 2 || wait(k_full + 1, 0));
         int done = 0, freed = 0;         // K_EMPTY, V_EMPTY commits issued
         if (ok) {
-          if (shorts) {
-            fix(wk, L::kK);
-            fix(wv, L::kV);
-            if (n_tiles > 1) fix(wk, L::kK + L::kTile);
-          }
           tc_fence_after();
           product_nt<D>(region(0), aQ, kmajor(sK(0)));
           commit(L::S_FULL);
@@ -465,9 +451,8 @@ __device__ __forceinline__ void dq_unit(const BwdTcParams<MP>& prm, int unit, ui
           if (s2 == 0) phk ^= 1;
           const uint32_t tS = tmem + 128 * r, tP = tmem + 128 * (r == 2 ? 0 : r + 1);
           if (j + 1 < n_tiles) {
-            ok = wait(L::V_FULL + (b ^ 1), (j + 1) / kVStages) && wait(L::S_READ + b, ph);
+            ok = wait(v_full + (b ^ 1), (j + 1) / kVStages) && wait(L::S_READ + b, ph);
             if (!ok) break;
-            if (shorts) fix(wv, L::kV + (b ^ 1) * L::kTile);
             tc_fence_after();
             product_nt<D>(tS, aO, kmajor(base + L::kV + (b ^ 1) * L::kTile));       // dP(j + 1) over S(j)
             commit(L::V_EMPTY + (b ^ 1));
@@ -481,8 +466,7 @@ __device__ __forceinline__ void dq_unit(const BwdTcParams<MP>& prm, int unit, ui
           ++done;
           if (j + 2 < n_tiles) {
             // K(j + 2) takes the stage of K(j - 1), which dQ(j - 1) has just released: dQ(j) covers the load
-            if (!(ok = wait(L::K_FULL + s2, phk))) break;
-            if (shorts) fix(wk, L::kK + s2 * L::kTile);
+            if (!(ok = wait(k_full + s2, phk))) break;
             tc_fence_after();
             product_nt<D>(tP, aQ, kmajor(base + L::kK + s2 * L::kTile));            // S(j + 2) over dS(j)
             commit(L::S_FULL + b);
@@ -493,6 +477,18 @@ __device__ __forceinline__ void dq_unit(const BwdTcParams<MP>& prm, int unit, ui
         }
         for (int i = max(0, done - kKStages); i < done; ++i) mbar_drain(bar(L::K_EMPTY + i % kKStages), (i / kKStages) & 1);
         for (int i = max(0, freed - kVStages); i < freed; ++i) mbar_drain(bar(L::V_EMPTY + i % kVStages), (i / kVStages) & 1);
+      }
+    } else if (warp == 2 && shorts) {
+      // ---------------------------------------------------------------- rows behind short ranges
+      int j = 0;
+      for (TileWalk w(t, g); w.valid(); w.next(), ++j) {
+        const int s = j % kKStages, u = j % kVStages;
+        if (!mbar_wait_warp(bar(L::K_FULL + s), (j / kKStages) & 1, abort_flag, status)) break;
+        if (w.is_short()) zero_rows<D>(gbase + L::kK + s * L::kTile, w.last(), lane);
+        mbar_arrive(bar(L::K_FIXED + s));
+        if (!mbar_wait_warp(bar(L::V_FULL + u), (j / kVStages) & 1, abort_flag, status)) break;
+        if (w.is_short()) zero_rows<D>(gbase + L::kV + u * L::kTile, w.last(), lane);
+        mbar_arrive(bar(L::V_FIXED + u));
       }
     }
   } else {

@@ -23,17 +23,6 @@ __device__ __forceinline__ int box_row(int t, int s0, int s1) {
   return (t + kRows > s1 && s1 - kRows >= s0) ? s1 - kRows : t;
 }
 
-template <typename Tables>
-__device__ __forceinline__ int count_tiles(const Tables& t, int g) {
-  int n = 0;
-  for (int p = 0; p < t.P;) {
-    int s0, s1;
-    p = next_range(t, g, p, s0, s1);
-    n += (s1 - s0 + kRows - 1) / kRows;
-  }
-  return n;
-}
-
 // Walks the 128-row tiles of the ranges that group g streams.
 template <typename Tables>
 struct TileWalk {
@@ -63,15 +52,14 @@ __device__ __forceinline__ void load_tile(uint32_t dst, const CUtensorMap* m, in
   for (int a = 0; a < D / 64; ++a) tma_load_3d(dst + a * kAtomBytes, m, a * 64, row, bh, bar);
 }
 
-// Zero rows [from, 128) of a tile (the thread that then issues the products that read it).  A row
-// of an atom is 128 contiguous bytes whatever the swizzle.
+// Zero rows [from, 128) of a tile (a warp, whose lanes then arrive on the barrier that the issuer of
+// the products waits on).  A row of an atom is 128 contiguous bytes whatever the swizzle.
 template <int D>
-__device__ __forceinline__ void zero_rows(uint8_t* tile, int from) {
+__device__ __forceinline__ void zero_rows(uint8_t* tile, int from, int lane) {
 #pragma unroll 1
-  for (int i = 0; i < (kRows - from) * (D / 64) * 8; ++i) {
-    const int c = i % 8, r = from + i / 8 % (kRows - from), a = i / 8 / (kRows - from);
-    *reinterpret_cast<uint4*>(tile + a * kAtomBytes + r * 128 + c * 16) = make_uint4(0u, 0u, 0u, 0u);
-  }
+  for (int i = from * 8 + lane; i < kRows * 8; i += 32)
+#pragma unroll
+    for (int a = 0; a < D / 64; ++a) *reinterpret_cast<uint4*>(tile + a * kAtomBytes + i * 16) = make_uint4(0u, 0u, 0u, 0u);
   fence_async_smem();
 }
 

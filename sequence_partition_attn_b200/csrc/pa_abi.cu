@@ -699,7 +699,7 @@ static int fill_owner_tiles(pa::AttnTables& t, int tile_rows) {
 
 }  // extern "C"
 
-// Launch order of the bf16 backward pass's units: groups that stream the most tokens first (ties in
+// Launch order of the bf16 backward pass's units: groups that stream the most tiles first (ties in
 // group order), all heads and tiles of a group together, which share what they stream.
 template <int MP>
 static bool fill_units(pa::BwdSide<MP>& side, const pa::AttnTables& t, long long BH) {
@@ -708,14 +708,17 @@ static bool fill_units(pa::BwdSide<MP>& side, const pa::AttnTables& t, long long
   side.QG = t.QG;
   memcpy(side.part_off, t.part_off, sizeof(int) * (t.P + 1));
   memcpy(side.qg_row0, t.qg_row0, sizeof(int) * (t.QG + 1));
-  long long tokens[MP];
   for (int g = 0; g < t.QG; ++g) {
     memcpy(side.fresh_bits[g], t.fresh_bits[g], sizeof side.fresh_bits[g]);
-    tokens[g] = 0;
-    for (int p = 0; p < t.P; ++p)
-      if (pa::fresh_bit(t.fresh_bits, g, p)) tokens[g] += t.part_off[p + 1] - t.part_off[p];
+    side.tiles[g] = side.shorts[g] = 0;
+    for (int p = 0; p < t.P;) {
+      int s0, s1;
+      p = pa::next_range(t, g, p, s0, s1);
+      side.tiles[g] += (s1 - s0 + tile - 1) / tile;
+      if (s1 > s0 && s1 - s0 < tile) side.shorts[g] = 1;
+    }
     int i = g;
-    for (; i > 0 && tokens[side.order[i - 1]] < tokens[g]; --i) side.order[i] = side.order[i - 1];
+    for (; i > 0 && side.tiles[side.order[i - 1]] < side.tiles[g]; --i) side.order[i] = side.order[i - 1];
     side.order[i] = static_cast<uint8_t>(g);
   }
   long long acc = 0;

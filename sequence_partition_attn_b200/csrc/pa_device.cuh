@@ -393,6 +393,8 @@ struct BwdSide {
   int qg_row0[MP + 1];
   int unit_start[MP + 1];         // by place in the order
   uint32_t fresh_bits[MP][kWords];
+  int tiles[MP];                  // that a group streams
+  uint8_t shorts[MP];             // some of its ranges are shorter than a tile
   uint8_t order[MP];
 };
 
@@ -468,7 +470,7 @@ __device__ __forceinline__ void e4m3_to_f16(uint32_t codes, uint32_t& lo, uint32
 // The maximal run of selected partitions at or after `from` that holds tokens, as the token
 // range [s0, s1) (neighbouring partitions join); returns where to go on.  s0 == s1 at the end.
 template <typename Tables>
-__device__ __forceinline__ int next_range(const Tables& t, int g, int from, int& s0, int& s1) {
+__host__ __device__ __forceinline__ int next_range(const Tables& t, int g, int from, int& s0, int& s1) {
   s0 = s1 = 0;
   int p = from;
   auto selected = [&](int i) { return (t.fresh_bits[g][i >> 5] >> (i & 31)) & 1u; };

@@ -119,7 +119,34 @@ def put_all(region, what):
 
 
 # ------------------------------------------------------------------ backward, dK and dV
-def kv_roles(T, q_stages=3, o_stages=2):
+def fixer(T, first, second, stages, ready):
+    """Warp 2 where ranges are shorter than a tile: rewrites each tile (modelled as for every one)."""
+    for j in range(T):
+        for name, n in ((first, stages[0]), (second, stages[1])):
+            s = j % n
+            yield ("wait", f"{name}_FULL{s}", j // n)
+            yield ("get", f"{name}{s}", (name, j))
+            yield ("put", f"{name}{s}", (ready[name], j))
+            yield ("arrive", f"{name}_FIXED{s}")
+
+
+def with_fixer(roles, need, T, first, second, stages):
+    """The same roles when warp 2 stands between the loads and the issuer."""
+    ready = {first: first + "*", second: second + "*"}
+
+    def issuer(ops):
+        for op in ops:
+            if op[0] == "wait" and op[1][:-1] in (f"{first}_FULL", f"{second}_FULL"):
+                op = ("wait", op[1].replace("FULL", "FIXED"), op[2])
+            elif op[0] == "mma":
+                op = ("mma", [(b, (ready[w[0]], w[1])) if w[0] in ready and isinstance(w, tuple) else (b, w) for b, w in op[1]], op[2])
+            yield op
+    roles = dict(roles, issuer=issuer(roles["issuer"]), fixer=fixer(T, first, second, stages, ready))
+    base = dict(need, **{ready[n]: need[n] for n in ready}, **{first: 1, second: 1})
+    return roles, lambda buf, what: base[what[0]]
+
+
+def kv_roles(T, q_stages=3, o_stages=2, shorts=False):
     def producer():
         yield ("load", "K", "K", "KV_FULL")
         yield ("load", "V", "V", "KV_FULL")
@@ -192,11 +219,14 @@ def kv_roles(T, q_stages=3, o_stages=2):
     counts = {"KV_FULL": 2, "P_LO": 2, "P_HI": 2, "DS_FULL": 2, "STAT_EMPTY0": 2, "STAT_EMPTY1": 2}
     need = {"Q": 2, "O": 3, "S": 1, "P": 1, "dP": 1, "dS": 1, "T": 2}
     roles = dict(producer=producer(), issuer=issuer(), terms=terms(), wg0=threads(0), wg1=threads(1))
+    if shorts:
+        roles, needs = with_fixer(roles, need, T, "Q", "O", (q_stages, o_stages))
+        return roles, counts, needs
     return roles, counts, lambda buf, what: need[what[0]]
 
 
 # ------------------------------------------------------------------ backward, dQ
-def q_roles(T, k_stages=3, v_stages=2):
+def q_roles(T, k_stages=3, v_stages=2, shorts=False):
     def region(i):
         return [(f"R{i % 3}", w) for w in range(2)]
 
@@ -262,6 +292,9 @@ def q_roles(T, k_stages=3, v_stages=2):
     counts = {"OWN_FULL": 2, **{f"{n}{b}": 2 for n in ("S_READ", "DS_FULL") for b in range(2)}}
     need = {"K": 2, "V": 1, "S": 1, "dP": 1, "dS": 1}
     roles = dict(producer=producer(), issuer=issuer(), wg0=threads(0), wg1=threads(1))
+    if shorts:
+        roles, needs = with_fixer(roles, need, T, "K", "V", (k_stages, v_stages))
+        return roles, counts, needs
     return roles, counts, lambda buf, what: need[what[0]]
 
 
@@ -334,10 +367,11 @@ def cache_roles(T, nx, stages=2):
 
 
 @pytest.mark.parametrize("T", list(range(1, 20)))
-@pytest.mark.parametrize("kind", ["kv", "q", "cache1", "cache2"])
+@pytest.mark.parametrize("kind", ["kv", "q", "kv-short", "q-short", "cache1", "cache2"])
 def test_protocol(kind, T):
     for seed in range(20):
-        roles, counts, need = {"kv": lambda: kv_roles(T), "q": lambda: q_roles(T), "cache1": lambda: cache_roles(T, 1),
+        roles, counts, need = {"kv": lambda: kv_roles(T), "q": lambda: q_roles(T), "kv-short": lambda: kv_roles(T, shorts=True),
+                               "q-short": lambda: q_roles(T, shorts=True), "cache1": lambda: cache_roles(T, 1),
                                "cache2": lambda: cache_roles(T, 2)}[kind]()
         m = simulate(roles, counts, need, seed)
         assert not m.open
