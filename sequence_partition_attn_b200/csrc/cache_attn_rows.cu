@@ -13,8 +13,10 @@
 // units (request, KV head, 16-row tile) in a row are cut into equal shares, one per resident
 // block of threads, so one launch is one full wave whatever the lengths.  A share may begin and
 // end inside a unit; each piece writes its state in fp32 to a slot of its own and the join adds a
-// unit's pieces in order, so results do not depend on the order in which blocks run.  (Equal numbers of splits per request instead: a batch with lengths
-// from 0 to 4096 took 26 us for 55 MB, nearly half of it on the longest request's blocks.)
+// unit's pieces in order, so results do not depend on the order in which blocks run.  (Equal
+// numbers of splits per request instead: a batch with lengths from 0 to 4096 took 26 us for 55 MB,
+// nearly half of it on the longest request's blocks.)  Short caches are not cut: blocks take whole
+// units, and there is no join.
 //
 // Each warp takes 16 tokens of every block and runs two tiles ahead with TMA loads into a ring of
 // its own: no barrier between warps in the loop, 128 KB in flight per SM.  (Plain and asynchronous
@@ -605,6 +607,37 @@ __global__ void __launch_bounds__(kWarps * 32, resident<T>(NT)) cache_attn_rows_
   }
 }
 
+// Short caches: a block takes whole units, and there is nothing to join.
+template <typename T, int D, int NT>
+__global__ void __launch_bounds__(kWarps * 32, resident<T>(NT)) cache_attn_short_kernel(const __grid_constant__ CacheAttnRowsParams par) {
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ Shared sh;
+  const CacheAttnParams& prm = par.c;
+  uint8_t* smem = smem_raw + (1024u - smem_u32(smem_raw) % 1024u) % 1024u;
+  if (threadIdx.x < kWarps * kStages) mbar_init(smem_u32(&sh.full[0][0]) + 8u * threadIdx.x, 1);
+  if (threadIdx.x == 0) sh.abort_flag = 0;
+  fence_mbar_init();
+  __syncthreads();
+  Slot into, from;
+  const long long of_request = static_cast<long long>(prm.Hk) * prm.row_tiles;
+  for (long long unit = blockIdx.x; unit < of_request * prm.B; unit += gridDim.x) {
+    const int b = static_cast<int>(unit / of_request);
+    const int len = cache_len(prm, b);
+    if (len > 0) {
+      if (!attend_piece<T, D, NT>(par, smem, sh, into, from, unit, len, 0, (len + PA_CACHE_BLOCK - 1) / PA_CACHE_BLOCK, -1)) return;
+      continue;
+    }
+    const long long bh = unit / prm.row_tiles;
+    const int row0 = static_cast<int>(unit - bh * prm.row_tiles) * 8 * NT;
+    const size_t at = static_cast<size_t>(bh) * prm.R + row0;
+    const int rows = min(8 * NT, prm.R - row0);
+    for (int i = threadIdx.x; i < rows * D / 4; i += kWarps * 32) {
+      store4(static_cast<T*>(prm.o) + at * D + 4 * i, make_float4(0.f, 0.f, 0.f, 0.f));
+      if (i < rows) prm.lse[at + i] = -INFINITY;
+    }
+  }
+}
+
 // ------------------------------------------------------------------ join
 // kWide: one block of 8 warps per query row, which take turns at the pieces, for few rows with many
 // pieces; else one warp per row.  A lane holds D / 32 channels.  The weighted sums are taken in
@@ -691,7 +724,14 @@ template <typename T, int D, int NT>
 int rows_impl(const CacheAttnRowsParams& par, cudaStream_t st) {
   constexpr int smem = Ring<D>::kBytes;
   const CacheAttnParams& prm = par.c;
-  cudaError_t e = cudaFuncSetAttribute(cache_attn_rows_kernel<T, D, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  cudaError_t e;
+  if (prm.slot_rows == 0) {
+    e = cudaFuncSetAttribute(cache_attn_short_kernel<T, D, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return static_cast<int>(e);
+    cache_attn_short_kernel<T, D, NT><<<prm.shares, kWarps * 32, smem, st>>>(par);
+    return static_cast<int>(cudaGetLastError());
+  }
+  e = cudaFuncSetAttribute(cache_attn_rows_kernel<T, D, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return static_cast<int>(e);
   cache_attn_rows_kernel<T, D, NT><<<prm.shares, kWarps * 32, smem, st>>>(par);
   if ((e = cudaGetLastError()) != cudaSuccess) return static_cast<int>(e);

@@ -884,6 +884,13 @@ static int pa_cache_store_impl(pa_ctx* ctx, const pa_cache_store_desc* d, void* 
 // (the last: so many splits that joining them costs as much as the attention).
 static bool cache_attn_many_rows(pa_dtype dtype, long long rows) { return dtype == PA_BF16 && rows > 32; }
 
+// Few query rows take a cache of at most this many blocks unit by unit: one launch without a join.
+// Longer ones are cut into equal shares.  us on a B200, whole units against shares:
+//   tokens                           64        256         512         1024        2048
+//    1 x  8 heads, D = 128       3.5/6.6    5.1/8.6     7.4/9.8    12.0/9.7    20.8/9.7
+//   16 x 24 heads, D = 128       4.8/8.9   7.7/11.4   11.0/14.7   17.5/17.9   32.0/26.6
+constexpr int kShortCache = 8;
+
 // Sizes and the split of the token axis of pa_cache_attn: a rule on sizes alone, so that the
 // scratch can be sized beforehand and a captured call replays with other lengths.
 static int plan_cache_attn(pa_ctx* ctx, pa_dtype dtype, int B, int H, int Hk, int Nq, int M, int D,
@@ -912,8 +919,13 @@ static int plan_cache_attn(pa_ctx* ctx, pa_dtype dtype, int B, int H, int Hk, in
   if (!cache_attn_many_rows(dtype, R)) {
     const int tile = pa::cache_attn_rows_tile_rows(prm.R, dtype);
     prm.row_tiles = (prm.R - 1) / tile + 1;
-    prm.slot_rows = std::min(prm.R, tile);
     prm.shares = ctx->sm_count * pa::cache_attn_rows_resident(prm.R, dtype);
+    if (prm.blocks <= kShortCache) {
+      prm.slot_rows = 0;
+      prm.shares = static_cast<int>(std::min<long long>(prm.shares, BHk * prm.row_tiles));
+      return PA_OK;
+    }
+    prm.slot_rows = std::min(prm.R, tile);
     *ws_bytes = 2 * static_cast<size_t>(prm.shares) * prm.slot_rows * (D + 1) * sizeof(float);
     return PA_OK;
   }

@@ -441,7 +441,7 @@ struct CacheAttnParams {
   int B, Hk, R, M, D, blocks;
   int splits;                     // of the token axis
   int row_tiles, shares;          // few rows: 16-row tiles per KV head, equal shares of the work,
-  int slot_rows;                  // rows of a scratch slot (two slots per share)
+  int slot_rows;                  // rows of a scratch slot (two slots per share); 0: blocks take whole units
   float scale;
 };
 
