@@ -319,10 +319,11 @@ typedef struct {
 } pa_cache_store_desc;
 
 /* Store rows at tokens [start[b], start[b] + T) of request b's cache, as a prompt or a token
- * at a time.  In a block that holds tokens before start[b], the scale becomes the larger of its
- * own and the new rows' one, and the older codes are rounded again if it grew; tokens at or
- * behind start[b] + T are not read and keep their codes, but not their meaning (the scale of
- * the last block they share is replaced).  A start outside [0, M - T] leaves that request's cache as it was
+ * at a time.  Tokens before start[b] in the first block that the rows touch must have been stored:
+ * that block's scale becomes the larger of its own and the new rows' one, and the older codes are
+ * rounded again if it grew.  Tokens at or behind start[b] + T are not read and keep their codes, but
+ * not their meaning (the scale of the last block they share is replaced).  A start outside
+ * [0, M - T] leaves that request's cache as it was
  * and records PA_EINVAL in the context's status word (pa_sync_status returns it).
  * Errors: PA_EINVAL, PA_EALIGN, PA_EUNSUPPORTED, PA_ECUDA. */
 int pa_cache_store(pa_ctx* ctx, const pa_cache_store_desc* desc, void* stream);
