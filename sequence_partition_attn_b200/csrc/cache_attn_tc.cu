@@ -51,7 +51,7 @@ struct Layout {
   static constexpr int kBar = kCodes + 4 * kItem;
   enum { Q_FULL = 0, K_FULL = 1, V_FULL = K_FULL + kStages, K_EMPTY = V_FULL + kStages,
          V_EMPTY = K_EMPTY + kStages, S_FULL = V_EMPTY + kStages, P_LO = S_FULL + 2, P_HI = P_LO + 2,
-         O_FINAL = P_HI + 2, NBAR = O_FINAL + 2 };
+         O_FINAL = P_HI + 2, O_READY = O_FINAL + 2, NBAR = O_READY + 2 };
   static constexpr int kSlot = kBar + NBAR * 8;
   static constexpr int kAbort = kSlot + 8;
   static constexpr int kBytes = kAbort + 8 + 1024;
@@ -171,7 +171,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attn_tc_kernel(const __grid
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < L::NBAR; ++i) {
-      const bool threads = (i >= L::K_FULL && i < L::K_EMPTY) || (i >= L::P_LO && i < L::O_FINAL);
+      const bool threads = (i >= L::K_FULL && i < L::K_EMPTY) || (i >= L::P_LO && i < L::O_FINAL) || i >= L::O_READY;
       mbar_init(bar(i), threads ? 128u : 1u);
     }
     *abort_flag = 0;
@@ -204,7 +204,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attn_tc_kernel(const __grid
       auto wait = [&](int b, uint32_t parity) { return mbar_wait(bar(b), parity, abort_flag, status); };
       auto commit = [&](int b) { mma_commit(bar(b)); };
       const uint64_t dq[2] = {tiles::kmajor(base + L::kQ), tiles::kmajor(base + L::kQ + L::kTile)};
-      bool ok = wait(L::Q_FULL, 0) && wait(L::K_FULL, 0) && wait(L::V_FULL, 0);
+      bool ok = wait(L::Q_FULL, 0) && wait(L::K_FULL, 0);
       if (ok) {
         tc_fence_after();
         for (int x = 0; x < nx; ++x) {
@@ -212,6 +212,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attn_tc_kernel(const __grid
           commit(L::S_FULL + x);
         }
         commit(L::K_EMPTY);
+        ok = wait(L::V_FULL, 0);
       }
       int done = 0;
       for (int j = 0; ok && j < T; ++j) {
@@ -329,17 +330,30 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attn_tc_kernel(const __grid
 #pragma unroll
           for (int i = 0; i < 16; ++i) v[i] = 0.0f;
         }
-        if (!row_ok) continue;
         if (prm.splits > 1) {
+          if (!row_ok) continue;
 #pragma unroll
           for (int i = 0; i < 16; i += 4) store4(prm.ws_o + at * D + c * 16 + i, make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]));
-        } else {
-          uint4* o = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(prm.o) + at * D + c * 16);
-          o[0] = make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]));
-          o[1] = make_uint4(pack_bf16x2(v[8], v[9]), pack_bf16x2(v[10], v[11]), pack_bf16x2(v[12], v[13]), pack_bf16x2(v[14], v[15]));
+        } else {                         // over Q_x, whose last product is done
+          uint8_t* o = gbase + L::kQ + x * L::kTile + (c >> 2) * kAtomBytes + row * 128;
+          const int ch = (c & 3) * 2, sw = row & 7;
+          *reinterpret_cast<uint4*>(o + ((ch ^ sw) << 4)) =
+              make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]));
+          *reinterpret_cast<uint4*>(o + (((ch + 1) ^ sw) << 4)) =
+              make_uint4(pack_bf16x2(v[8], v[9]), pack_bf16x2(v[10], v[11]), pack_bf16x2(v[12], v[13]), pack_bf16x2(v[14], v[15]));
         }
       }
       if (row_ok) (prm.splits > 1 ? prm.ws_lse : prm.lse)[at] = T > 0 ? (m + fast_log2(l)) * kLn2 : -INFINITY;
+      if (prm.splits == 1) {
+        fence_async_smem();
+        mbar_arrive(bar(L::O_READY + x));
+        // rows behind the head's last are not written
+        if (row == 0 && mbar_wait(bar(L::O_READY + x), 0, abort_flag, status)) {
+          for (int a = 0; a < D / 64; ++a)
+            tma_store_3d(&p.tm_o, base + L::kQ + x * L::kTile + a * kAtomBytes, a * 64, row0 + x * kBM, bh);
+          tma_store_wait();
+        }
+      }
     }
   } else {
     // ---------------------------------------------------------------- widening

@@ -979,6 +979,7 @@ static int pa_cache_attn_impl(pa_ctx* ctx, const pa_cache_attn_desc* d, void* st
     tc.row_blocks = (prm.R - 1) / pa::cache_attn_tc_block_rows() + 1;
     tc.scale_log2 = d->scale * 1.4426950408889634f;
     if ((rc = encode_qkv_map(ctx, &tc.tm_q, d->q, d->B * d->Hk, prm.R, d->D))) return rc;
+    if ((rc = encode_qkv_map(ctx, &tc.tm_o, d->o, d->B * d->Hk, prm.R, d->D))) return rc;
     const long long units = static_cast<long long>(d->B) * d->Hk * tc.row_blocks * prm.splits;
     if (units > 0x7fffffffLL) return fail(ctx, PA_EINVAL, "too many work units");
     e = pa::launch_cache_attn_tc(tc, static_cast<unsigned>(units), st);

@@ -186,6 +186,17 @@ __device__ __forceinline__ void tma_prefetch(const CUtensorMap* m) {
   asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(m)) : "memory");
 }
 
+// Box of shared memory to a tensor (rows outside it are not written), and the wait until all of the
+// thread's stores are done.
+__device__ __forceinline__ void tma_store_3d(const CUtensorMap* m, uint32_t src, int x, int y, int z) {
+  asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group [%0, {%2, %3, %4}], [%1];" ::"l"(m), "r"(src), "r"(x),
+               "r"(y), "r"(z)
+               : "memory");
+}
+__device__ __forceinline__ void tma_store_wait() {
+  asm volatile("cp.async.bulk.commit_group;\n\tcp.async.bulk.wait_group 0;" ::: "memory");
+}
+
 // 3-D tiled load into this CTA's own shared memory, completing `bar`'s transaction count.
 __device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* m, int x, int y,
                                             int z, uint32_t bar) {
@@ -451,7 +462,7 @@ struct CacheAttnRowsParams {
 };
 
 struct CacheAttnTcParams {
-  CUtensorMap tm_q;               // {D, R, B * Hk}
+  CUtensorMap tm_q, tm_o;         // {D, R, B * Hk}
   CacheAttnParams c;
   int row_blocks;                 // 256-row blocks per KV head
   float scale_log2;

@@ -300,7 +300,7 @@ def q_roles(T, k_stages=3, v_stages=2, shorts=False):
 
 # ------------------------------------------------------------------ attention over the cache
 def cache_roles(T, nx, stages=2):
-    """nx query tiles.  A score region is two halves, which P is handed over in; (max, sum) go over Q."""
+    """nx query tiles.  A score region is two halves, which P is handed over in; O leaves over Q."""
     def loader():
         for x in range(nx):
             yield ("load", f"Q{x}", "Q", "Q_FULL")
@@ -311,11 +311,11 @@ def cache_roles(T, nx, stages=2):
     def issuer():
         yield ("wait", "Q_FULL", 0)
         yield ("wait", "K_FULL0", 0)
-        yield ("wait", "V_FULL0", 0)
         for x in range(nx):
             yield score(x, 0)
             yield ("commit", f"S_FULL{x}")
         yield ("commit", "K_EMPTY0")
+        yield ("wait", "V_FULL0", 0)
         for j in range(T):
             s, s1, more = j % stages, (j + 1) % stages, j + 1 < T
             for x in range(nx):
@@ -345,8 +345,8 @@ def cache_roles(T, nx, stages=2):
             for h, bar in ((0, "P_LO"), (1, "P_HI")):
                 yield ("put", (f"S{x}", h), ("P", j))
                 yield ("arrive", f"{bar}{x}")
-        yield ("put", f"Q{x}", "ML")
-        yield ("arrive", f"ML_FULL{x}")
+        yield ("wait", f"O_FINAL{x}", 0)
+        yield ("put", f"Q{x}", "O")
 
     def widen():
         for j in range(T):
@@ -356,10 +356,6 @@ def cache_roles(T, nx, stages=2):
                     yield ("wait", f"{kv}_EMPTY{s}", j // stages - 1)
                 yield ("put", f"{kv}{s}", (kv, j))
                 yield ("arrive", f"{kv}_FULL{s}")
-        for x in range(nx):
-            yield ("wait", f"O_FINAL{x}", 0)
-            yield ("wait", f"ML_FULL{x}", 0)
-            yield ("get", f"Q{x}", "ML")
 
     need = {"K": nx, "V": 2 * nx, "S": 1, "P": 1, "Q": T}
     roles = dict(loader=loader(), issuer=issuer(), widen=widen(), **{f"softmax{x}": softmax(x) for x in range(nx)})
