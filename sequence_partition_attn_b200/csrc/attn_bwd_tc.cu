@@ -255,7 +255,6 @@ __device__ __forceinline__ void dkdv_unit(const BwdTcParams<MP>& prm, int unit, 
     // ---------------------------------------------------------------- P and dS, then the stores
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsHigh));
     const int x = (warp - 4) >> 2;                    // columns 64 x .. 64 x + 63
-    const int row = (warp & 3) * 32 + lane;
     const uint32_t lane_off = static_cast<uint32_t>((warp & 3) * 32) << 16;
     const uint32_t sX = tX + lane_off + x * 64, sY = tY + lane_off + x * 64;
     const float2 scale2 = make_float2(prm.scale_log2, prm.scale_log2);
@@ -316,16 +315,18 @@ __device__ __forceinline__ void dkdv_unit(const BwdTcParams<MP>& prm, int unit, 
       mbar_arrive(bar(L::DS_FULL));
       mbar_arrive(bar(L::STAT_EMPTY + slot));
     }
-    // warpgroup 0 stores dV, warpgroup 1 dK
+    // warpgroup 0 stores dV, warpgroup 1 dK; over K and V, whose last products are done
+    const int row0 = (warp & 3) * 32;
     __nv_bfloat16* out = static_cast<__nv_bfloat16*>(x ? prm.dk : prm.dv) +
-                         (static_cast<size_t>(bh) * prm.N + own0 + row) * D;
-    const bool row_ok = own0 + row < own1;
+                         (static_cast<size_t>(bh) * prm.N + own0 + row0) * D;
+    const int rows = own1 - own0 - row0;               // of this warp's 32
     if (n_tiles == 0) {
-      if (row_ok)
-        for (int c = 0; c < D / 8; ++c) reinterpret_cast<uint4*>(out)[c] = make_uint4(0, 0, 0, 0);
-    } else if (ok && mbar_wait(bar(L::FINAL), 0, abort_flag, status)) {
+      if (lane < rows)
+        for (int c = 0; c < D / 8; ++c) reinterpret_cast<uint4*>(out + lane * D)[c] = make_uint4(0, 0, 0, 0);
+    } else if (__all_sync(0xffffffffu, ok) && mbar_wait_warp(bar(L::FINAL), 0, abort_flag, status)) {
       tc_fence_after();
-      store_rows<D>((x ? tDK : tDV) + lane_off, out, x ? prm.scale : 1.0f, row_ok);
+      store_rows<D, D>((x ? tDK : tDV) + lane_off, gbase + L::kK + x * L::kTile + row0 * 2 * D, out,
+                       x ? prm.scale : 1.0f, rows, lane);
     }
   }
 
@@ -545,14 +546,18 @@ __device__ __forceinline__ void dq_unit(const BwdTcParams<MP>& prm, int unit, ui
       store_weights(region(2 * j + 1) + lane_off, ds);
       mbar_arrive(bar(L::DS_FULL + (j & 1)));
     }
-    // each warpgroup stores half of dQ's columns
-    __nv_bfloat16* out = static_cast<__nv_bfloat16*>(prm.dq) + at * D + x * (D / 2);
+    // each warpgroup stores half of dQ's columns, over Q, whose last product is done
+    const int row0 = (warp & 3) * 32;
+    __nv_bfloat16* out = static_cast<__nv_bfloat16*>(prm.dq) +
+                         (static_cast<size_t>(bh) * prm.N + own0 + row0) * D + x * (D / 2);
+    const int rows = own1 - own0 - row0;
     if (n_tiles == 0) {
-      if (row_ok)
-        for (int c = 0; c < D / 16; ++c) reinterpret_cast<uint4*>(out)[c] = make_uint4(0, 0, 0, 0);
-    } else if (ok && mbar_wait(bar(L::FINAL), 0, abort_flag, status)) {
+      if (lane < rows)
+        for (int c = 0; c < D / 16; ++c) reinterpret_cast<uint4*>(out + lane * D)[c] = make_uint4(0, 0, 0, 0);
+    } else if (__all_sync(0xffffffffu, ok) && mbar_wait_warp(bar(L::FINAL), 0, abort_flag, status)) {
       tc_fence_after();
-      store_rows<D / 2>(tDQ + (lane_off & 0xFFFF0000u) + x * (D / 2), out, prm.scale, row_ok);
+      store_rows<D / 2, D>(tDQ + (lane_off & 0xFFFF0000u) + x * (D / 2), gbase + L::kQ + x * (L::kTile / 2) + row0 * D, out,
+                           prm.scale, rows, lane);
     }
   }
 
