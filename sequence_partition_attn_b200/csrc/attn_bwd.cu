@@ -206,6 +206,7 @@ __device__ __forceinline__ void bwd_unit(const BwdParams& prm, int tile, uint8_t
       }
       split_store<S::kOwnPlane>(smem + S::kOwnAt + x * 3 * S::kOwnPlane, S::kRow, r, c, a, b);
     }
+  asm volatile("griddepcontrol.wait;" ::: "memory");           // delta is written
   float lse_own[2] = {INFINITY, INFINITY}, delta_own[2] = {0.0f, 0.0f};    // rows gid, gid + 8 (dQ)
   if (kDq)
 #pragma unroll
@@ -386,8 +387,17 @@ int f32_impl(const BwdParams& prm, cudaStream_t st) {
   constexpr int smem = Shape<D, kOwn>::kBytes;
   cudaError_t e = cudaFuncSetAttribute(attn_bwd_f32_kernel<D, kOwn>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return static_cast<int>(e);
-  attn_bwd_f32_kernel<D, kOwn><<<dim3(prm.tiles_k + prm.tiles_q, prm.BH), kThreads, smem, st>>>(prm);
-  return static_cast<int>(cudaGetLastError());
+  cudaLaunchConfig_t cfg = {};             // ahead of the end of the delta kernel, which its blocks wait for
+  cfg.gridDim = dim3(prm.tiles_k + prm.tiles_q, prm.BH);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr = {};
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return static_cast<int>(cudaLaunchKernelEx(&cfg, attn_bwd_f32_kernel<D, kOwn>, prm));
 }
 
 template <typename T, int D>
