@@ -70,9 +70,10 @@ def test_many_partitions(ctx, dtype, P, G):
 
 # ------------------------------------------------------------------ many requests and rows
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
-@pytest.mark.parametrize("B,H,Hk,Nq", [(70, 2, 2, 1), (33, 6, 2, 3), (2, 2, 1, 150), (3, 1, 1, 33)])
-def test_many_requests_and_rows(ctx, dtype, B, H, Hk, Nq):
-    M, D = 300, 64
+@pytest.mark.parametrize("M", [300, 700])                  # whole units, and shares of them
+@pytest.mark.parametrize("B,H,Hk,Nq", [(70, 2, 2, 1), (33, 6, 2, 3), (2, 2, 1, 150), (3, 1, 1, 33), (40, 24, 24, 1)])
+def test_many_requests_and_rows(ctx, dtype, B, H, Hk, Nq, M):
+    D = 64
     lens = [int(x) for x in np.random.default_rng(B).integers(0, M + 1, B)]
     lens[0], lens[-1] = 0, M
     cache = make_cache(ctx, B, Hk, M, D, 40 + B)
