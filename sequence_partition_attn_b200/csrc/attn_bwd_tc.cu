@@ -54,8 +54,16 @@ __device__ __forceinline__ void read_scores(uint32_t tmem, float (&s)[64]) {
 // The group, head and first row of a unit: groups in launch order, heads and then tiles in each.
 template <int MP>
 __device__ __forceinline__ int owner_tile(const BwdSide<MP>& side, int unit, int& bh, int& own0) {
-  int i = 0;
-  while (side.unit_start[i + 1] <= unit) ++i;
+  int i = 0;      // the last place that starts at or before the unit (those without rows end there)
+  for (int n = side.QG; n > 1;) {
+    const int half = n / 2;
+    if (side.unit_start[i + half] <= unit) {
+      i += half;
+      n -= half;
+    } else {
+      n = half;
+    }
+  }
   const int g = side.order[i];
   const int rows = side.qg_row0[g + 1] - side.qg_row0[g];
   const int tiles = (rows + kRows - 1) / kRows;
