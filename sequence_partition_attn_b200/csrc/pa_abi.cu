@@ -709,7 +709,13 @@ static bool fill_units(pa::BwdSide<MP>& side, const pa::AttnTables& t, long long
   memcpy(side.part_off, t.part_off, sizeof(int) * (t.P + 1));
   memcpy(side.qg_row0, t.qg_row0, sizeof(int) * (t.QG + 1));
   for (int g = 0; g < t.QG; ++g) {
-    memcpy(side.fresh_bits[g], t.fresh_bits[g], sizeof side.fresh_bits[g]);
+    memset(side.fresh_bits[g], 0, sizeof side.fresh_bits[g]);
+    for (int p = 0; p < t.P; ++p) {
+      const bool empty = t.part_off[p + 1] == t.part_off[p];
+      const bool on = empty ? p > 0 && ((side.fresh_bits[g][(p - 1) >> 5] >> ((p - 1) & 31)) & 1u)
+                            : pa::fresh_bit(t.fresh_bits, g, p);
+      if (on) side.fresh_bits[g][p >> 5] |= 1u << (p & 31);
+    }
     side.tiles[g] = side.shorts[g] = 0;
     for (int p = 0; p < t.P;) {
       int s0, s1;

@@ -403,7 +403,7 @@ struct BwdSide {
   int part_off[MP + 1];
   int qg_row0[MP + 1];
   int unit_start[MP + 1];         // by place in the order
-  uint32_t fresh_bits[MP][kWords];
+  uint32_t fresh_bits[MP][kWords];  // of empty partitions: as the one before (0 for the first)
   int tiles[MP];                  // that a group streams
   uint8_t shorts[MP];             // some of its ranges are shorter than a tile
   uint8_t order[MP];
@@ -491,6 +491,29 @@ __host__ __device__ __forceinline__ int next_range(const Tables& t, int g, int f
   while (p < t.P && (selected(p) || t.part_off[p + 1] == t.part_off[p])) ++p;
   s1 = t.part_off[p];
   return p;
+}
+
+// The same from a BwdSide, whose empty partitions carry the bit of the one before them: a run of
+// selected partitions is a run of set bits.  (The walk over single partitions took the producer of
+// the backward pass 1500 cycles for 8 of them, 2900 for 27, before its first load.)
+template <int MP>
+__device__ __forceinline__ int next_range(const BwdSide<MP>& t, int g, int from, int& s0, int& s1) {
+  constexpr int kWords = BwdSide<MP>::kWords;
+  s0 = s1 = 0;
+  if (from >= t.P) return t.P;
+  int w = from >> 5;
+  uint32_t set = t.fresh_bits[g][w] & (~0u << (from & 31));
+  while (set == 0) {
+    if (++w == kWords) return t.P;
+    set = t.fresh_bits[g][w];
+  }
+  const int a = w * 32 + __ffs(set) - 1;
+  uint32_t clear = ~t.fresh_bits[g][w] & (~0u << (a & 31));
+  while (clear == 0 && ++w < kWords) clear = ~t.fresh_bits[g][w];
+  const int b = clear ? min(w * 32 + __ffs(clear) - 1, t.P) : t.P;
+  s0 = t.part_off[a];
+  s1 = t.part_off[b];
+  return b;
 }
 
 // Tokens per split of a request of `len` tokens: whole cache blocks.
