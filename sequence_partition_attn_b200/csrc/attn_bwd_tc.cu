@@ -16,7 +16,7 @@
 // Roles (384 threads, one CTA per SM).  warp 0: TMA producer.  warp 1: TMEM owner and MMA issuer
 // (one thread).  warp 2, where a group streams a range shorter than a tile: zeroes the rows behind
 // it, which may hold anything, and passes every tile on to the issuer (22 x 10 tokens in 32
-// partitions: 28 us; 360 us with the issuing thread zeroing).  warp 3 (dK, dV): -LSE and -delta of
+// partitions: 20 us; 360 us with the issuing thread zeroing).  warp 3 (dK, dV): -LSE and -delta of
 // the streamed queries into shared memory.  warps
 // 4-7 and 8-11: two warpgroups, one TMEM lane per thread, columns 0-63 and 64-127 of the scores.
 // Launched at 168 registers: warpgroup 0 drops to 88, the others rise to 208.
