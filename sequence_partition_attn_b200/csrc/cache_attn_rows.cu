@@ -40,9 +40,10 @@
 //     weights that way: it takes bf16 (2^-8, any magnitude) instead.
 // fp32 queries take two f16 terms for each element of q and each weight (three bf16 ones in small
 // blocks): 22 bits, for twice the products and the same conversions.
-// The conversions (about 0.9 instructions per code) are what bounds a block of threads; with
-// queries as the 16 rows and V in bf16 throughout they were 1.6, and the kernel was held by them:
-// 64 us for the 236 MB of one 115200-token cache, 49% of the issue slots, 46% of DRAM.
+// The conversions (about 0.9 instructions per code) are most of the work: the 236 MB of one
+// 115200-token cache take 49 us (53 with the join), with the issue slots and the ALU half busy and
+// DRAM at 60%; what is left is the chain of a tile's steps in the 16 warps that registers allow.  With
+// queries as the 16 rows and V in bf16 throughout they were 1.6 per code: 64 us, 46% of DRAM.
 #include <cuda_fp16.h>
 
 #include "pa_device.cuh"
