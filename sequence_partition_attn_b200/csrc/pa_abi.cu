@@ -685,6 +685,17 @@ static int pa_relayout_seq2head_at_impl(pa_ctx* ctx, const void* src, void* dst,
   return e ? cuda_fail(ctx, e, "relayout launch") : PA_OK;
 }
 
+// Empty partitions take the bit of the one before them, as the backward pass's walk wants it.
+static void carry_over_empty(pa::AttnTables& t) {
+  for (int g = 0; g < t.QG; ++g)
+    for (int p = 0; p < t.P; ++p) {
+      if (t.part_off[p + 1] > t.part_off[p]) continue;
+      const uint32_t bit = 1u << (p & 31);
+      t.fresh_bits[g][p >> 5] &= ~bit;
+      if (p > 0 && pa::fresh_bit(t.fresh_bits, g, p - 1)) t.fresh_bits[g][p >> 5] |= bit;
+    }
+}
+
 // Row tiles of the backward pass per owner group.  Unlike the forward's, groups without a fresh
 // pair are kept: their gradients are written as zeros.
 static int fill_owner_tiles(pa::AttnTables& t, int tile_rows) {
@@ -709,13 +720,7 @@ static bool fill_units(pa::BwdSide<MP>& side, const pa::AttnTables& t, long long
   memcpy(side.part_off, t.part_off, sizeof(int) * (t.P + 1));
   memcpy(side.qg_row0, t.qg_row0, sizeof(int) * (t.QG + 1));
   for (int g = 0; g < t.QG; ++g) {
-    memset(side.fresh_bits[g], 0, sizeof side.fresh_bits[g]);
-    for (int p = 0; p < t.P; ++p) {
-      const bool empty = t.part_off[p + 1] == t.part_off[p];
-      const bool on = empty ? p > 0 && ((side.fresh_bits[g][(p - 1) >> 5] >> ((p - 1) & 31)) & 1u)
-                            : pa::fresh_bit(t.fresh_bits, g, p);
-      if (on) side.fresh_bits[g][p >> 5] |= 1u << (p & 31);
-    }
+    memcpy(side.fresh_bits[g], t.fresh_bits[g], sizeof side.fresh_bits[g]);
     side.tiles[g] = side.shorts[g] = 0;
     for (int p = 0; p < t.P;) {
       int s0, s1;
@@ -799,6 +804,8 @@ static int pa_attn_backward_impl(pa_ctx* ctx, const pa_attn_bwd_desc* d, void* s
       if (!d->fresh || d->fresh[(p / d->G) * tq.QG + kg]) tk.fresh_bits[kg][p >> 5] |= 1u << (p & 31);
   merge_equal_groups(tq);
   merge_equal_groups(tk);
+  carry_over_empty(tq);
+  carry_over_empty(tk);
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   int e = 0;
   if (d->dtype == PA_F32) {

@@ -480,25 +480,19 @@ __device__ __forceinline__ void e4m3_to_f16(uint32_t codes, uint32_t& lo, uint32
 
 // The maximal run of selected partitions at or after `from` that holds tokens, as the token
 // range [s0, s1) (neighbouring partitions join); returns where to go on.  s0 == s1 at the end.
+// Empty partitions carry the bit of the one before them (0 for the first), so a run of selected
+// partitions is a run of set bits.  (A walk over single partitions took the producer of the bf16
+// backward pass 1500 cycles for 8 of them, 2900 for 27, before its first load.)
+__host__ __device__ __forceinline__ int first_bit(uint32_t x) {      // of x != 0
+#ifdef __CUDA_ARCH__
+  return __ffs(x) - 1;
+#else
+  return __builtin_ctz(x);
+#endif
+}
 template <typename Tables>
 __host__ __device__ __forceinline__ int next_range(const Tables& t, int g, int from, int& s0, int& s1) {
-  s0 = s1 = 0;
-  int p = from;
-  auto selected = [&](int i) { return (t.fresh_bits[g][i >> 5] >> (i & 31)) & 1u; };
-  while (p < t.P && !(selected(p) && t.part_off[p + 1] > t.part_off[p])) ++p;
-  if (p == t.P) return p;
-  s0 = t.part_off[p];
-  while (p < t.P && (selected(p) || t.part_off[p + 1] == t.part_off[p])) ++p;
-  s1 = t.part_off[p];
-  return p;
-}
-
-// The same from a BwdSide, whose empty partitions carry the bit of the one before them: a run of
-// selected partitions is a run of set bits.  (The walk over single partitions took the producer of
-// the backward pass 1500 cycles for 8 of them, 2900 for 27, before its first load.)
-template <int MP>
-__device__ __forceinline__ int next_range(const BwdSide<MP>& t, int g, int from, int& s0, int& s1) {
-  constexpr int kWords = BwdSide<MP>::kWords;
+  constexpr int kWords = sizeof(t.fresh_bits[0]) / sizeof(uint32_t);
   s0 = s1 = 0;
   if (from >= t.P) return t.P;
   int w = from >> 5;
@@ -507,10 +501,11 @@ __device__ __forceinline__ int next_range(const BwdSide<MP>& t, int g, int from,
     if (++w == kWords) return t.P;
     set = t.fresh_bits[g][w];
   }
-  const int a = w * 32 + __ffs(set) - 1;
+  const int a = w * 32 + first_bit(set);
   uint32_t clear = ~t.fresh_bits[g][w] & (~0u << (a & 31));
   while (clear == 0 && ++w < kWords) clear = ~t.fresh_bits[g][w];
-  const int b = clear ? min(w * 32 + __ffs(clear) - 1, t.P) : t.P;
+  int b = t.P;
+  if (clear != 0 && w * 32 + first_bit(clear) < b) b = w * 32 + first_bit(clear);
   s0 = t.part_off[a];
   s1 = t.part_off[b];
   return b;
