@@ -260,11 +260,35 @@ def prepare(case, seed):
         if case["op"] == "backward":
             st["out"] = [torch.empty_like(st["q"]) for _ in range(3)]
             st["delta"] = torch.empty_like(st["lse"])
+        elif case["op"] == "cache_store":
+            _keep_older(st)
         elif case["op"] == "cache_attn":
             st["o"] = torch.empty_like(st["q"])
             st["lse"] = torch.empty(st["q"].shape[:3], device="cuda")
             st["ws"] = pa.cache_attn_workspace(st["ctx"], st["q"], st["kc"])
     return st
+
+
+def _keep_older(st):
+    """The older tokens of the blocks that the rows begin in, and those blocks' scales: the call
+    rounds them again in place, and every pass has to meet them as they were.  K's and V's codes
+    (and scales) are halves of one tensor, which is put back at once."""
+    codes = torch.stack([st[c].view(torch.uint8) for c in ("kc", "vc")])
+    scale = torch.stack([st[c] for c in ("ks", "vs")])
+    st["kc"], st["vc"] = (x.view(torch.float8_e4m3fn) for x in codes)
+    st["ks"], st["vs"] = scale
+    _, B, Hk, M, D = codes.shape
+    heads = torch.arange(2 * B * Hk, device="cuda").view(2, B, Hk)
+    rows, blocks = [], []
+    for b, t0 in enumerate(_starts(st["case"])):
+        if t0 % BLOCK:
+            held = torch.arange(t0 // BLOCK * BLOCK, t0, device="cuda")
+            rows.append((heads[:, b].reshape(-1, 1) * M + held).flatten())
+            blocks.append(heads[:, b].flatten() * scale.shape[3] + t0 // BLOCK)
+    st["older"] = []
+    if rows:
+        for flat, at in ((codes.view(-1, D), torch.cat(rows)), (scale.view(-1), torch.cat(blocks))):
+            st["older"].append((flat, at, flat[at]))
 
 
 # ------------------------------------------------------------------ the operators
@@ -280,6 +304,8 @@ def _run_own(st):
                             st["case"]["G"], st["fresh"], dq, dk, dv, st["delta"], dlse=st["dlse"])
         return {"dq": dq, "dk": dk, "dv": dv}
     if op == "cache_store":
+        for flat, at, held in st["older"]:          # as the plain form, from the cache as it was given
+            flat.index_copy_(0, at, held)
         pa.pa_cache_store(ctx, st["k"], st["v"], st["start"], st["kc"], st["vc"], st["ks"], st["vs"])
         return {"kc": st["kc"], "ks": st["ks"], "vc": st["vc"], "vs": st["vs"]}
     pa.pa_cache_attn(ctx, st["q"], st["kc"], st["vc"], st["ks"], st["vs"], st["lens"], st["o"], st["lse"],
