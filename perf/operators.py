@@ -251,12 +251,18 @@ def _inputs(case, seed):
     return st
 
 
+_contexts = {}          # by device: a program keeps one for all its calls
+
+
 def prepare(case, seed):
     st = _inputs(case, seed)
     if own:
         import sequence_partition_attn_b200 as pa
         st["pa"] = pa
-        st["ctx"] = pa.Context(torch.cuda.current_device())
+        device = torch.cuda.current_device()
+        if device not in _contexts:
+            _contexts[device] = pa.Context(device)
+        st["ctx"] = _contexts[device]
         if case["op"] == "backward":
             st["out"] = [torch.empty_like(st["q"]) for _ in range(3)]
             st["delta"] = torch.empty_like(st["lse"])
