@@ -652,9 +652,9 @@ __global__ void __launch_bounds__(kJoinWarps * 32) cache_attn_rows_join_kernel(c
   __shared__ float s_sum[kJoinWarps], s_acc[kJoinWarps][D];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const long long row = kWide ? blockIdx.x : static_cast<long long>(blockIdx.x) * kJoinWarps + warp;
-  if (row >= prm.rows) return;
-  const long long bh = row / prm.R;
-  const int r = static_cast<int>(row - bh * prm.R);
+  const long long of = min(row, prm.rows - 1);                  // rows behind the last set up for it, and wait
+  const long long bh = of / prm.R;
+  const int r = static_cast<int>(of - bh * prm.R);
   const int b = static_cast<int>(bh / prm.Hk);
   Requests req(prm, lane);
   const Share share = work_share(prm, req);
@@ -665,11 +665,13 @@ __global__ void __launch_bounds__(kJoinWarps * 32) cache_attn_rows_join_kernel(c
                           (unit - static_cast<long long>(b) * prm.Hk * prm.row_tiles) * unit_places(nb) + kPieceCost;
   // shares that hold a piece of the unit
   const long long p0 = first / share.size, p1 = (first + nb - 1) / share.size;
-  if (nb > 0 && p0 == p1) return;
+  // The pieces are written.  Every thread waits, also one without a piece to join: what comes next in
+  // the stream is ordered behind this kernel only, so it must not end before the first has.
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  if (row >= prm.rows || (nb > 0 && p0 == p1)) return;
   const int pieces = nb > 0 ? static_cast<int>(p1 - p0 + 1) : 0;
   // piece i's row in the scratch: the first piece starts the unit, the others go on with it
   auto at = [&](int i) { return static_cast<size_t>(2 * (p0 + i) + (i == 0)) * prm.slot_rows + r % tile_rows; };
-  asm volatile("griddepcontrol.wait;" ::: "memory");           // the pieces are written
 
   constexpr int kStep = kWide ? kJoinWarps : 1;
   const int start = kWide ? warp : 0;
