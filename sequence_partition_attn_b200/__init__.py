@@ -16,6 +16,7 @@ raise.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 import struct
@@ -367,6 +368,17 @@ def _raw_stream(ctx, stream):
     return stream if isinstance(stream, int) else stream.cuda_stream
 
 
+def _allocating_for(ctx, stream):
+    """Torch allocates for the stream of this handle.  Memory comes from what was freed for the same
+    stream, whose work may still use it, and goes back there: right for work on that stream only."""
+    torch = _torch()
+    if stream == torch._C._cuda_getCurrentRawStream(ctx.device):
+        return contextlib.nullcontext()
+    # 0 is the default stream; as an external handle torch would take it for "none given"
+    return torch.cuda.stream(torch.cuda.ExternalStream(stream, device=ctx.device) if stream
+                             else torch.cuda.default_stream(ctx.device))
+
+
 def pa_attn_backward(ctx: Context, q, k, v, o, lse, do, part_off, G, fresh, dq, dk, dv, delta,
                      dlse=None, scale=None, stream=None):
     """Gradients dq, dk, dv (overwritten, [B, H, N, D]) of the fresh pairs of a merged output
@@ -439,7 +451,7 @@ def pa_cache_attn(ctx: Context, q, kc, vc, k_scale, v_scale, lens, o, lse, scale
     """Attention state (o [B, H, Nq, D], lse [B, H, Nq] f32) of q against the first lens[b]
     tokens (int32 [B] on the device, or None for all M) of the 8-bit cache; H is a multiple of
     the cache's Hk.  workspace: from cache_attn_workspace; without one the call takes it from
-    torch's allocator."""
+    torch's allocator, for the stream it runs on."""
     torch = _torch()
     B, Hk, M, D, pk, pv, pks, pvs = _cache_args(ctx, kc, vc, k_scale, v_scale)
     _, H, Nq, _ = _four("q", q)
@@ -447,10 +459,8 @@ def pa_cache_attn(ctx: Context, q, kc, vc, k_scale, v_scale, lens, o, lse, scale
     pq = _want(ctx, "q", q, rows, dt)
     s = _raw_stream(ctx, stream)
     if workspace is None:
-        workspace = cache_attn_workspace(ctx, q, kc)
-        if workspace.numel():
-            # allocated for the current stream: not handed out again before `s` is done with it
-            workspace.record_stream(torch.cuda.ExternalStream(s, device=workspace.device))
+        with _allocating_for(ctx, s):
+            workspace = cache_attn_workspace(ctx, q, kc)
     size = workspace.numel()
     d = _CACHE_ATTN.pack(_code(q), B, H, Hk, Nq, M, D, _scale(scale, D), pq, pk, pv, pks, pvs,
                          _maybe(ctx, "lens", lens, (B,), torch.int32), _want(ctx, "o", o, rows, dt),
