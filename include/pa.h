@@ -86,7 +86,8 @@
  * Validation happens before anything is enqueued: on error nothing was launched.
  * Device-side waits are bounded; a wait that gives up records PA_ETIMEOUT in the
  * context's status word, which pa_sync_status reads (and clears).  So does a cache length or
- * offset in device memory that lies outside the cache (PA_EINVAL).
+ * offset in device memory that lies outside the cache (PA_EINVAL); of several the gravest is
+ * kept, a wait that gave up before all others.
  *
  * Alignment.  q, k, v, o_part, o, gradients, cache codes, cache scratch and relayout src/dst
  * must be 16-byte aligned; lse_part, lse, w, delta, cache scales, lengths and offsets 4-byte

@@ -77,7 +77,7 @@ __device__ __forceinline__ int owner_tile(const BwdSide<MP>& side, int unit, int
 // room to move the base).  Checked, and recorded if it ever does not.
 __device__ __forceinline__ bool smem_aligned(uint32_t base, int* status) {
   if ((base & 1023u) == 0) return true;
-  if (threadIdx.x == 0) atomicExch(status, PA_ECUDA);
+  if (threadIdx.x == 0) record_status(status, PA_ECUDA);
   return false;
 }
 

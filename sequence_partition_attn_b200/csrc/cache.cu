@@ -120,7 +120,7 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 8 : 5) cache_store_
   const int b = bh / prm.Hk;
   const int t0 = prm.start ? prm.start[b] : 0;
   if (t0 < 0 || t0 > prm.M - prm.T) {                  // the rows do not fit: leave the request's cache alone
-    if (threadIdx.x == 0) atomicExch(prm.status, PA_EINVAL);
+    if (threadIdx.x == 0) record_status(prm.status, PA_EINVAL);
     return;
   }
   const int blk = t0 / kTok + i;

@@ -132,6 +132,10 @@ __device__ __forceinline__ bool mbar_try_wait(uint32_t bar, uint32_t parity) {
   return ok != 0;
 }
 
+// Record `code` in the context status word unless a graver one is there: the codes are negative, a
+// wait that gave up (results are missing) is the lowest and a bad length or offset the highest.
+__device__ __forceinline__ void record_status(int* status, int code) { atomicMin(status, code); }
+
 // A device-side wait never spins for ever: after kWaitLimitNs it records PA_ETIMEOUT in
 // the context status word, raises the block's abort flag (so every other role stops at
 // its next wait) and returns false.
@@ -146,7 +150,7 @@ __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, volatil
     if (*abort_flag) return false;
     if (globaltimer_ns() - t0 > limit_ns) {
       *abort_flag = 1;
-      atomicExch(status, PA_ETIMEOUT);
+      record_status(status, PA_ETIMEOUT);
       return false;
     }
   }
@@ -522,7 +526,7 @@ __device__ __forceinline__ int cache_len(const CacheAttnParams& prm, int b) {
   if (!prm.lens) return prm.M;
   const int n = prm.lens[b];
   if (n >= 0 && n <= prm.M) return n;
-  atomicExch(prm.status, PA_EINVAL);
+  record_status(prm.status, PA_EINVAL);
   return n < 0 ? 0 : prm.M;
 }
 
