@@ -135,7 +135,8 @@ const char* pa_last_error(const pa_ctx* ctx);
 
 /* Synchronise `stream`, then read and clear the context's device status word.
  * Returns PA_OK, PA_ETIMEOUT if a kernel's bounded wait gave up, PA_EINVAL if a cache length
- * or offset in device memory was out of range, or PA_ECUDA. */
+ * or offset in device memory was out of range, or PA_ECUDA (a CUDA error, or a kernel that did
+ * not run because its shared memory was not placed as it needs). */
 int pa_sync_status(pa_ctx* ctx, void* stream);
 
 /* pa_sync_status with a host-side deadline: poll `stream` (cudaStreamQuery) for up to

@@ -375,7 +375,9 @@ static int read_status(pa_ctx* ctx) {
   if (h != 0) {
     cudaMemset(ctx->d_status, 0, sizeof(int));
     if (h == PA_EINVAL) return fail(ctx, PA_EINVAL, "a cache length or offset in device memory is outside the cache");
-    return fail(ctx, PA_ETIMEOUT, "a device-side wait gave up (status %d)", h);
+    if (h == PA_ETIMEOUT) return fail(ctx, PA_ETIMEOUT, "a device-side wait gave up (status %d)", h);
+    if (h == PA_ECUDA) return fail(ctx, PA_ECUDA, "a kernel's shared memory did not start on the boundary that its tiles need");
+    return fail(ctx, PA_ECUDA, "unknown status %d", h);
   }
   return PA_OK;
 }

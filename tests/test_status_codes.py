@@ -41,3 +41,12 @@ def test_a_wait_that_gave_up_outweighs_a_bad_length(call, order):
     with pytest.raises(pa.PAError, match="PA_EINVAL"):
         ctx.sync_status()
     ctx.close()
+
+
+def test_every_recorded_code_is_reported_as_itself():
+    recorded = set()
+    for path in glob.glob(os.path.join(CSRC, "*.cu")) + glob.glob(os.path.join(CSRC, "*.cuh")):
+        recorded |= set(re.findall(r"record_status\([^;]*\b(PA_E\w+)\)", open(path).read()))
+    assert recorded >= {"PA_ETIMEOUT", "PA_EINVAL"}
+    read = re.search(r"static int read_status\(.*?\n}\n", open(os.path.join(CSRC, "pa_abi.cu")).read(), re.S).group(0)
+    assert recorded == set(re.findall(r"h == (PA_E\w+)\) return fail\(ctx, \1,", read))
