@@ -39,7 +39,8 @@
 //     weight where that is more.  A block whose scale is below 2^-16 of vmax would lose small
 //     weights that way: it takes bf16 (2^-8, any magnitude) instead.
 // fp32 queries take two f16 terms for each element of q and each weight (three bf16 ones in small
-// blocks): 22 bits, for twice the products and the same conversions.
+// blocks): 22 bits, for twice the products and the same conversions.  O errs by 1e-7 to 1e-6 of its
+// norm (512 to 131072 tokens; plain fp32 sums: the same), up to 3e-6 where scores reach 20.
 // The conversions (about 0.9 instructions per code) are most of the work: the 236 MB of one
 // 115200-token cache take 49 us (53 with the join), with the issue slots and the ALU half busy and
 // DRAM at 60%; what is left is the chain of a tile's steps in the 16 warps that registers allow.  With
@@ -219,6 +220,7 @@ __device__ __forceinline__ bool attend_piece(const CacheAttnRowsParams& par, uin
   const CacheAttnParams& prm = par.c;
   constexpr bool kF32 = sizeof(T) == 4;
   constexpr int kTerms = kF32 ? 2 : 1;   // f16 terms of q and of the weights
+  static_assert(!kF32 || NT == 1, "fp32 sums by the tile hold one column block");
   constexpr int kRows = 8 * NT;
   constexpr int kSteps = D / 16;         // k-steps of S^T; 16-channel blocks of O^T
   using R = Ring<D>;
@@ -430,6 +432,22 @@ __device__ __forceinline__ bool attend_piece(const CacheAttnRowsParams& par, uin
         if (partial && tok + xg + 8 * (e >> 1) >= end) p[c][e] = 0.0f;     // also where -inf meets a scale of 0
         l[c][e & 1] += p[c][e];
       }
+    // fp32: a tile's products start from zero and are added to O in fp32.  The tensor cores cut their
+    // sums, an error of one sign that grows with the tokens (4 heads x 512 queries x 131072 tokens: 7e-5 of
+    // O; added 2e-7, as plain fp32 sums, for 1% of the time).
+    float part[2][4];
+    auto sum = [&](int c, int b) -> float (&)[4] { return kF32 ? part[b & 1] : o[c][b]; };
+    auto clear_sums = [&]() {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) part[0][e] = part[1][e] = 0.0f;
+    };
+    auto add_sums = [&](int w) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        o[0][2 * w][e] += part[0][e];
+        o[0][2 * w + 1][e] += part[1][e];
+      }
+    };
     const float unit = kUnit * ratio;
     if (ratio >= kSmallScale || !(ratio > 0.0f)) {
       uint32_t pb[kTerms][NT][2];
@@ -455,13 +473,15 @@ __device__ __forceinline__ bool attend_piece(const CacheAttnRowsParams& par, uin
         e4m3_to_f16(hi01, a[2], a[3]);
         e4m3_to_f16(lo23, b[0], b[1]);
         e4m3_to_f16(hi23, b[2], b[3]);
+        if (kF32) clear_sums();
 #pragma unroll
         for (int c = 0; c < NT; ++c)
 #pragma unroll
           for (int e = 0; e < kTerms; ++e) {
-            mma_f16(o[c][2 * w], a, pb[e][c]);
-            mma_f16(o[c][2 * w + 1], b, pb[e][c]);
+            mma_f16(sum(c, 2 * w), a, pb[e][c]);
+            mma_f16(sum(c, 2 * w + 1), b, pb[e][c]);
           }
+        if (kF32) add_sums(w);
       }
     } else {
       constexpr int kWide = kF32 ? 3 : 1;
@@ -493,13 +513,15 @@ __device__ __forceinline__ bool attend_piece(const CacheAttnRowsParams& par, uin
           a[i] = to_bf16(a[i]);
           b[i] = to_bf16(b[i]);
         }
+        if (kF32) clear_sums();
 #pragma unroll
         for (int c = 0; c < NT; ++c)
 #pragma unroll
           for (int e = 0; e < kWide; ++e) {
-            mma_bf16(o[c][2 * w], a, pb[e][c]);
-            mma_bf16(o[c][2 * w + 1], b, pb[e][c]);
+            mma_bf16(sum(c, 2 * w), a, pb[e][c]);
+            mma_bf16(sum(c, 2 * w + 1), b, pb[e][c]);
           }
+        if (kF32) add_sums(w);
       }
     }
   }
