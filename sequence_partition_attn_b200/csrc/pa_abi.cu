@@ -906,6 +906,12 @@ static bool cache_attn_many_rows(pa_dtype dtype, long long rows) { return dtype 
 //   16 x 24 heads, D = 128       4.8/8.9   7.7/11.4   11.0/14.7   17.5/17.9   32.0/26.6
 constexpr int kShortCache = 8;
 
+// Cache blocks that one block of threads of the tcgen05 kernel sums at most: 131072 tokens.  The tensor
+// cores cut a sum by up to 2^-23 for each 16 tokens, always the same way: 2^-10 of O over this many, a
+// quarter of bf16's rounding.  (38400 rows x 1048576 tokens, D = 64: O 6.0e-3 too small in one piece, 5e-4
+// in eight with 80 MB of scratch; 25.8 and 14.6 ms, as 150 blocks of threads were two waves.)
+constexpr int kMaxChain = 131072 / PA_CACHE_BLOCK;
+
 // Sizes and the split of the token axis of pa_cache_attn: a rule on sizes alone, so that the
 // scratch can be sized beforehand and a captured call replays with other lengths.
 static int plan_cache_attn(pa_ctx* ctx, pa_dtype dtype, int B, int H, int Hk, int Nq, int M, int D,
@@ -948,6 +954,8 @@ static int plan_cache_attn(pa_ctx* ctx, pa_dtype dtype, int B, int H, int Hk, in
   const long long tiles = BHk * ((R - 1) / tile_rows + 1);
   // enough blocks to fill the GPU, each with a few cache blocks of tokens
   prm.splits = static_cast<int>(std::max(1LL, std::min(ctx->sm_count / tiles, static_cast<long long>(prm.blocks) / 4)));
+  // and none with more than kMaxChain blocks, whose sums the tensor cores would cut too often
+  prm.splits = std::max(prm.splits, (prm.blocks - 1) / kMaxChain + 1);
   if (prm.splits > 1) *ws_bytes = static_cast<size_t>(prm.splits) * prm.rows * (D + 1) * sizeof(float);
   return PA_OK;
 }

@@ -48,3 +48,36 @@ def test_fp32_sums_are_rounded_and_not_cut(D, far):
         assert float(err.max()) <= tol, (r, float(err.max()), tol)
         assert abs(float(lse[0, 0, r]) - float(torch.logsumexp(s, 0))) <= tol + 4 * bounds.U * 12
     ctx.close()
+
+
+def test_bf16_sums_over_a_million_tokens():
+    """So many rows that the token axis need not be cut to fill the GPU.  The tensor cores cut their sums
+    by up to 2^-23 for each 16 tokens; a chain of them is at most 131072 tokens long: 2^13 steps, 2^-10
+    of O.  The mean over the channels shows it under the output's rounding (2^-8, either sign, six
+    standard deviations of 64 uniform errors); flat scores, so that the weights' rounding averages out.
+    lse: a score errs by 2 D u sum|scale q k| (0.5), a sum of 1024 tiles by 6 sqrt(1024) u, the result by
+    4 u 14: below 2^-15 together."""
+    D, M, rows = 64, 1 << 20, 256 * 150
+    ctx = pa.Context(0)
+    g = torch.Generator(device="cuda").manual_seed(3)
+    kc, vc = (torch.empty(1, 1, M, D, dtype=torch.uint8, device="cuda") for _ in range(2))
+    ks, vs = (torch.empty(1, 1, M // 64, device="cuda") for _ in range(2))
+    k = torch.randn(1, 1, M, D, generator=g, device="cuda")
+    v = 1.0 + 0.9 * torch.rand(1, 1, M, D, generator=g, device="cuda")
+    v *= 1.0 + torch.arange(D, device="cuda") / D               # channels whose roundings are not alike
+    pa.pa_cache_store(ctx, k, v, None, kc, vc, ks, vs)
+    q = torch.randn(1, 1, rows, D, generator=g, device="cuda").mul_(0.1).to(torch.bfloat16)
+    o, lse = torch.full_like(q, float("nan")), torch.full((1, 1, rows), float("nan"), device="cuda")
+    pa.pa_cache_attn(ctx, q, kc, vc, ks, vs, None, o, lse)
+    ctx.sync_status()
+    kk, vv = (c[0, 0].view(torch.float8_e4m3fn).double() * s[0, 0].double().repeat_interleave(64)[:, None]
+              for c, s in ((kc, ks), (vc, vs)))
+    tol = 2.0 ** -10 + 6 * 2.0 ** -8 / (3 * D) ** 0.5 + 2.0 ** -15
+    for r in range(0, rows, 2500):
+        s = D ** -0.5 * (q[0, 0, r].double() @ kk.T)
+        want = torch.softmax(s, 0) @ vv
+        err = (o[0, 0, r].double() - want) / want
+        assert abs(float(err.mean())) <= tol, (r, float(err.mean()), tol)
+        assert float(err.abs().max()) <= 2.0 ** -8 + 2.0 ** -10 + 2.0 ** -15
+        assert abs(float(lse[0, 0, r]) - float(torch.logsumexp(s, 0))) <= 2.0 ** -15
+    ctx.close()
