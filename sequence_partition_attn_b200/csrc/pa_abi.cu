@@ -855,6 +855,7 @@ static int pa_cache_store_impl(pa_ctx* ctx, const pa_cache_store_desc* d, void* 
   if (d->D != 64 && d->D != 128) return fail(ctx, PA_EUNSUPPORTED, "D=%d (supported: 64, 128)", d->D);
   if (d->B < 1 || d->Hk < 1 || d->T < 0 || d->M < 1) return fail(ctx, PA_EINVAL, "B=%d Hk=%d T=%d M=%d", d->B, d->Hk, d->T, d->M);
   if (d->T > d->M) return fail(ctx, PA_EINVAL, "T=%d rows do not fit a cache of M=%d", d->T, d->M);
+  if (d->M > 0x7fffffff - 1024) return fail(ctx, PA_EINVAL, "M=%d too large", d->M);   // tok0 runs past M by a block
   if (d->T == 0) return PA_OK;
   if (!d->k || !d->v || !d->k_codes || !d->v_codes || !d->k_scale || !d->v_scale)
     return fail(ctx, PA_EINVAL, "null tensor pointer");
