@@ -16,8 +16,8 @@ from __future__ import annotations
 import numpy as np
 import torch
 
-from . import (Context, pa_attn_backward, pa_merge_states, pa_partition_attn, pa_relayout_seq2head,
-               pa_state_drift, predict_fresh, select_fresh)
+from . import (Context, _allocating_for, _raw_stream, pa_attn_backward, pa_merge_states,
+               pa_partition_attn, pa_relayout_seq2head, pa_state_drift, predict_fresh, select_fresh)
 
 
 def attn_flops(part_off, G: int, fresh, B: int, H: int, D: int) -> float:
@@ -64,7 +64,7 @@ class AttentionStep:
         self.lse_cached = mk(P, B, H, N, dt=torch.float32) if reuse else None
         self.o, self.lse = mk(B, H, N, D), mk(B, H, N, dt=torch.float32)
         self.w = mk(self.QG, P, dt=torch.float32)
-        self.delta = mk(B, H, N, dt=torch.float32)      # scratch of the backward pass
+        self.delta = None                               # scratch of the backward pass, from the first one on
         self.flops = attn_flops(self.part_off, G, self.fresh, B, H, D)
         self.merge_bytes = merge_bytes(B, H, N, D, P, torch.empty(0, dtype=dtype).element_size())
 
@@ -96,6 +96,9 @@ class AttentionStep:
         gradients do by o and dlse by lse (None: 0).  Reads o and lse as ``run`` left them (all
         five default to the step's own buffers).  Cached states count as constants: they hold
         no K and V to pass a gradient to.  Uses the step's scratch: one backward at a time."""
+        if self.delta is None:
+            with _allocating_for(self.ctx, _raw_stream(self.ctx, stream)):
+                self.delta = torch.empty_like(self.lse)
         pick = lambda given, own: own if given is None else given            # noqa: E731
         pa_attn_backward(self.ctx, pick(q, self.q), pick(k, self.k), pick(v, self.v),
                          pick(o, self.o), pick(lse, self.lse), do, self.part_off, self.G, self.fresh,
