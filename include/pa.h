@@ -354,7 +354,9 @@ typedef struct {
  * pa_partition_attn's states, so pa_merge_states joins it with others.  The scratch belongs to
  * the caller: calls that may overlap need one each.  A length outside [0, M] is
  * clamped and records PA_EINVAL in the context's status word.  Results do not depend on the
- * order in which blocks run.  Errors: PA_EINVAL, PA_EALIGN, PA_EUNSUPPORTED, PA_ECUDA. */
+ * order in which blocks run: the same call gives the same bits.  The token axis is cut where the
+ * sizes and lengths of the whole call say, so a request's last bits may differ in another batch.
+ * Errors: PA_EINVAL, PA_EALIGN, PA_EUNSUPPORTED, PA_ECUDA. */
 int pa_cache_attn(pa_ctx* ctx, const pa_cache_attn_desc* desc, void* stream);
 
 /* Bytes of scratch that pa_cache_attn needs for these sizes (0 when none), on this device. */
