@@ -56,13 +56,20 @@ namespace {
 constexpr int kWarps = 4;
 constexpr int kTok = 16;               // tokens per tile
 constexpr int kStages = 3;             // tiles in shared memory per warp
-constexpr int kPieceCost = 4;          // what a piece costs besides its blocks, in blocks
-constexpr int kMinPlaces = 6;          // places per share, at least
+// What a piece costs besides its blocks, in blocks.  us with 0 / 2 / 4 / 8: 8 x 24 heads of up to 4096
+// tokens 45 / 29.5 / 28.6 / 28.5, 64 x 8 heads of up to 2048 53.5 / 39.7 / 37.1 / 38.1.
+constexpr int kPieceCost = 4;
+// Places per share, at least.  us with 5 / 6 / 9 / 16: 8 heads x 1024 tokens 9.3 / 10.0 / 11.7 / 15.6,
+// 2 x 4 heads x 3000 tokens 9.4 / 9.4 / 10.7 / 13.8.
+constexpr int kMinPlaces = 6;
 static_assert(kWarps * kTok == PA_CACHE_BLOCK, "the warps share one cache block");
 constexpr float kUnit = 128.0f;        // weights are held as this times p vs / vmax
 constexpr float kSmallScale = 1.0f / 65536.0f;
 
-constexpr int kWideRows = 1024;        // query rows in all up to which the join takes a block per row
+// Query rows in all up to which the join takes a block of threads per row instead of a warp.  us, block
+// against warp: 40 rows x 115200 tokens 60 / 78, 256 rows x 8192 19.5 / 23.9, 1280 x 8192 47.3 / 45.4,
+// 2048 x 8192 70.5 / 65.0.
+constexpr int kWideRows = 1024;
 constexpr int kMaxRows = 16;           // queries per tile: NT columns of 8, NT = 1 or 2 (fp32: 1)
 template <typename T>
 __host__ __device__ constexpr int row_columns(int R) { return R <= 8 || sizeof(T) == 4 ? 1 : 2; }

@@ -829,9 +829,10 @@ static int pa_attn_backward_impl(pa_ctx* ctx, const pa_attn_bwd_desc* d, void* s
     prm.D = d->D;
     prm.scale = d->scale;
     // Blocks of 32 rows halve the time of one block and stream the other side twice as often: they
-    // are taken when all of them run at once.  us on a B200, 32 against 64 rows: 2 x 1024 x 64 (128
-    // blocks of 32 rows) 61 / 110, 4 x 1024 x 64 (256) 112 / 113, 2 x 1024 x 128 115 / 172,
-    // 4 x 1024 x 128 221 / 173.
+    // are taken when all of them run at once.  us on a B200, 32 against 64 rows: 1 x 512 x 64 (32
+    // blocks of 32 rows) 30 / 52, 2 x 1024 x 64 (128) 56 / 106, 2 x 1024 x 128 111 / 169,
+    // 4 x 1024 x 64 (256) 108 / 118, 8 x 512 x 64 59 / 64, 4 x 1024 x 128 217 / 172,
+    // 24 x 1536 x 64 1134 / 914.
     int own = 32;
     prm.tiles_q = fill_owner_tiles(prm.tq, own);
     prm.tiles_k = fill_owner_tiles(prm.tk, own);
@@ -892,19 +893,24 @@ static int pa_cache_store_impl(pa_ctx* ctx, const pa_cache_store_desc* d, void* 
 
 // bf16 queries take the tcgen05 kernel when a KV head has more than 32 query rows: it reads the codes
 // once for 256 rows, but takes 128-token tiles and 128 rows at the least, the other reads them once
-// for every 16 rows and wastes less on few.  us on a B200, D = 128, other kernel against tcgen05:
-//   rows                               16         32         48         64        128
-//   24 heads,  1 x 4096 tokens     17.4/22.3  21.5/22.1  26.8/22.4  30.3/22.1  46.6/23.7
-//    8 heads,  8 x 2048 tokens     20.5/24.2  25.0/24.2  30.5/24.6  36.1/24.4  59.8/27.2
-//    2 heads, 1 x 16384 tokens     14.2/26.0  16.5/25.7  18.3/25.9  18.9/23.1  23.9/27.6
-// (the last: so many splits that joining them costs as much as the attention).
+// for every 16 rows and wastes less on few.  us on a B200 with cold caches, D = 128, other kernel
+// against tcgen05:
+//   rows                                 16          32          48          64          128
+//   24 heads, 1 x 4096 tokens        19.1/24.1   23.4/24.2   29.0/24.7   32.4/24.8   49.4/26.2
+//    8 heads, 8 x 2048 tokens        22.8/25.2   27.1/25.4   33.0/25.8   39.0/26.2   64.8/28.8
+//    8 heads, 1 x 16384 tokens       20.7/29.3   25.3/30.2   31.6/30.5   36.0/30.6   60.4/31.8
+//    8 heads, 1 x 100000 tokens      55.9/96.2   92.2/97.1  116.3/97.2  149.3/97.3  279.9/98.7
+//    2 heads, 1 x 16384 tokens       15.1/25.1   17.0/26.7   19.9/26.8   20.1/26.2   24.3/29.1
+//    2 heads, 1 x 100000 tokens      28.4/46.1   35.2/47.0   43.5/47.5   49.6/46.6   79.4/49.5
+// The rule looks at the rows only.  With 2 heads of 16384 tokens it takes the slower kernel from 33 to
+// 128 rows: so many splits that joining them costs as much as the attention.
 static bool cache_attn_many_rows(pa_dtype dtype, long long rows) { return dtype == PA_BF16 && rows > 32; }
 
 // Few query rows take a cache of at most this many blocks unit by unit: one launch without a join.
-// Longer ones are cut into equal shares.  us on a B200, whole units against shares:
-//   tokens                           64        256         512         1024        2048
-//    1 x  8 heads, D = 128       3.5/6.6    5.1/8.6     7.4/9.8    12.0/9.7    20.8/9.7
-//   16 x 24 heads, D = 128       4.8/8.9   7.7/11.4   11.0/14.7   17.5/17.9   32.0/26.6
+// Longer ones are cut into equal shares.  us on a B200 with cold caches, whole units against shares:
+//   tokens                           64         256        512         1024        2048
+//    1 x  8 heads, D = 128       3.9/7.1    5.6/8.7     7.8/9.8   12.1/10.2   21.2/10.3
+//   16 x 24 heads, D = 128       5.9/9.4   9.7/15.0   15.8/19.4   25.6/29.4   44.8/49.8
 constexpr int kShortCache = 8;
 
 // Cache blocks that one block of threads of the tcgen05 kernel sums at most: 131072 tokens.  The tensor
@@ -953,7 +959,10 @@ static int plan_cache_attn(pa_ctx* ctx, pa_dtype dtype, int B, int H, int Hk, in
   }
   const int tile_rows = pa::cache_attn_tc_block_rows();
   const long long tiles = BHk * ((R - 1) / tile_rows + 1);
-  // enough blocks to fill the GPU, each with a few cache blocks of tokens
+  // enough blocks to fill the GPU, each with four cache blocks of tokens at least.  us on a B200, D = 128,
+  // at least 1 / 2 / 4 / 8 / 16: 2 heads x 128 rows x 2048 tokens 18.1 / 14.1 / 14.8 / 17.2 / 24.3,
+  // 8 x 256 x 1024 19.4 / 16.8 / 17.6 / 20.9 / 22.2, 1 x 256 x 8192 43.0 / 28.5 / 23.2 / 22.8 / 29.3,
+  // 4 x 64 x 16384 27.2 / 27.2 / 27.3 / 23.9 / 26.5.
   prm.splits = static_cast<int>(std::max(1LL, std::min(ctx->sm_count / tiles, static_cast<long long>(prm.blocks) / 4)));
   // and none with more than kMaxChain blocks, whose sums the tensor cores would cut too often
   prm.splits = std::max(prm.splits, (prm.blocks - 1) / kMaxChain + 1);

@@ -398,8 +398,8 @@ struct BwdParams {
 
 // Owners of row tiles in the bf16 backward pass: their groups with the partitions they stream, and
 // the launch order of the units (group, head, tile): groups with the most to stream first.  Sized
-// by the number of partitions, up to 32 or up to PA_MAX_P: the parameters of a launch are then 1.5
-// or 7 KB, and the smaller launch is microseconds sooner on its way.
+// by the number of partitions, up to 32 or up to PA_MAX_P: the parameters of a launch are then 2
+// or 9 KB, and the smaller launch is microseconds sooner on its way.
 template <int MP>
 struct BwdSide {
   static constexpr int kWords = MP / 32;
@@ -426,6 +426,7 @@ struct BwdTcParams {
   float scale, scale_log2;
   BwdSide<MP> kv, q;
 };
+static_assert(sizeof(BwdTcParams<32>) <= 2048 && sizeof(BwdTcParams<PA_MAX_P>) <= 9 * 1024 + 128, "the sizes named above");
 
 struct CacheStoreParams {
   const void* k;                  // [B][Hk][T][D]
