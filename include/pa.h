@@ -307,7 +307,8 @@ int pa_attn_backward(pa_ctx* ctx, const pa_attn_bwd_desc* desc, void* stream);
  * block of PA_CACHE_BLOCK tokens and head, [B][Hk][ceil(M / PA_CACHE_BLOCK)]: the value of a
  * code is code * scale.  The scale is the smallest power of two 2^e with
  * amax <= 448 * 2^e (amax over the block's finite values), e >= -126, and 0 for a block of
- * zeros.  Infinities are stored as +-448, NaN stays NaN.  Neither needs initialising. */
+ * zeros.  An infinity is stored as the code +-448, the largest value of its block's scale (0 in a
+ * block without a finite value but zeros); NaN stays NaN.  Neither needs initialising. */
 typedef struct {
   pa_dtype dtype;            /* of k and v */
   int B, Hk, T, M, D;        /* T new tokens into a cache of M (T <= M), D in {64, 128} */
@@ -348,11 +349,16 @@ typedef struct {
 
 /* Attention state of each query row against the first lens[b] tokens of its request's cache:
  *   lse_i = ln sum_j exp(scale q_i . k_j),  o_i = sum_j exp(scale q_i . k_j - lse_i) v_j.
- * Query head h reads KV head h / (H / Hk).  The scales are powers of two or 0, as pa_cache_store
+ * Query head h reads KV head h / (H / Hk).  There is no causal mask: all Nq rows of a request see the
+ * same tokens, so causal decoding takes Nq = 1.  The scales are powers of two or 0, as pa_cache_store
  * leaves them.  Tokens at or behind lens[b] and the scales of blocks behind it have no influence,
  * whatever they hold; without any token o = 0, lse = -inf.  The result has the layout of one of
- * pa_partition_attn's states, so pa_merge_states joins it with others.  The scratch belongs to
- * the caller: calls that may overlap need one each.  A length outside [0, M] is
+ * pa_partition_attn's states, so pa_merge_states joins it with others.  Sums and softmax statistics
+ * are fp32.  fp32 queries: O errs by 1e-7 to 1e-6 of its norm, as plain fp32 sums.  bf16: weights are
+ * rounded to bf16 (few rows: mostly f16), and the tensor cores cut O's sum by up to 2^-23 for each 16
+ * tokens (many rows, chains of at most 131072) or 64 (few rows): 2^-10 of O at 131072 tokens, against
+ * 2^-8 of the output's own rounding.  The scratch belongs to the caller: calls that may overlap need
+ * one each.  The outputs may not overlap the inputs.  A length outside [0, M] is
  * clamped and records PA_EINVAL in the context's status word.  Results do not depend on the
  * order in which blocks run: the same call gives the same bits.  The token axis is cut where the
  * sizes and lengths of the whole call say, so a request's last bits may differ in another batch.

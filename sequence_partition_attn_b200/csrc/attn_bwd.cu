@@ -54,7 +54,7 @@ __global__ void __launch_bounds__(256) delta_kernel(const T* __restrict__ o, con
 // cannot overflow), x1 the rest rounded and x2 what is left, off by 2^-25 of x.  A product of two values takes
 // the six terms x0y0, x0y1, x1y0, x1y1, x0y2, x2y0; the others are below 2^-22 of it, and the sums
 // are fp32.  That is six bf16 products for one, at the tensor cores' rate: 24 x 1536 x 128, all
-// pairs, takes 1.82 ms (56 fp32 TFLOP/s executed, 334 of bf16), and 2 x 1024 x 64 takes 54 us.  The
+// pairs, takes 1.82 ms (56 fp32 TFLOP/s executed, 334 of bf16), and 2 x 1024 x 64 takes 55 us.  The
 // packed multiply-add units took 2.70 ms and 106 us.  Bound by the tensor cores' warp products,
 // then by the shared-memory reads of their operands (about 3/4 of the products' time).
 //

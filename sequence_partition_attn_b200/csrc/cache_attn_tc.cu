@@ -9,8 +9,8 @@
 // products read.  The scale is a power of two, so code * scale is exact in bf16: nothing is
 // rounded that the cache did not round already, and the scores need no scale of their own.
 // The codes cross HBM and L2 in 8 bits; a pass that widened the cache to bf16 first would write
-// and read it again at twice the size.  40 heads x 9450 queries x 9450 tokens, D = 128: 1.6 ms, a
-// tile of 128 tokens every 3800 cycles, of which the softmax warps work 2200 and wait for the
+// and read it again at twice the size.  40 heads x 9450 queries x 9450 tokens, D = 128: 1.77 ms
+// at the power cap, 1.56 ms before it is reached, a tile of 128 tokens every 3800 cycles, of which the softmax warps work 2200 and wait for the
 // products between.  (Loads into registers one block ahead: 1.93 ms, as L2 answers in about a
 // thousand cycles and a tile has four of them in a row.  f16 tiles with the scales in the softmax
 // instead: fewer instructions to widen, but 500 more per tile in the softmax, which sets the pace.)
