@@ -450,7 +450,8 @@ def pa_cache_attn(ctx: Context, q, kc, vc, k_scale, v_scale, lens, o, lse, scale
                   stream=None):
     """Attention state (o [B, H, Nq, D], lse [B, H, Nq] f32) of q against the first lens[b]
     tokens (int32 [B] on the device, or None for all M) of the 8-bit cache; H is a multiple of
-    the cache's Hk.  workspace: from cache_attn_workspace; without one the call takes it from
+    the cache's Hk.  No causal mask: all Nq rows of a request see the same tokens.
+    workspace: from cache_attn_workspace; without one the call takes it from
     torch's allocator, for the stream it runs on."""
     torch = _torch()
     B, Hk, M, D, pk, pv, pks, pvs = _cache_args(ctx, kc, vc, k_scale, v_scale)
